@@ -394,6 +394,86 @@ typedef struct {
 int mpt_check_flat_noalloc(const void* d_grads_half, int64_t n, float scale, float clip,
                            mpt_check_result* d_result, void* cuda_stream);
 
+/* ---- gradient lists: global norm and clipping ----------------------------
+ *
+ * The norm and the clipping of mpt_step for gradients that do not go (or not
+ * at once) through mpt_step: lists of FP16, BF16 or FP32 tensors, mixed as
+ * they come, of any element-aligned address and any size, zero included.
+ *
+ *   s_i  = sum of g^2 over tensor i           (binary64)
+ *   norm = sqrt(sum of s_i) / S               tensor norm i = sqrt(s_i) / S
+ *   coef = clip / norm, rounded to binary32, when clip > 0, every gradient is
+ *          finite and norm > clip; else 1
+ *   out  = T(fp32(g) * coef), or with MPT_LIST_UNSCALE
+ *          T(fp32(g) * fp32(1/S) * coef); each product rounded to binary32,
+ *          T = the output type's round-to-nearest-even
+ *
+ * A gradient that is +-inf or NaN makes found_inf 1, the norm (and its
+ * tensor's norm) +inf and the coefficient 1: the outputs are then the
+ * gradients themselves (unscaled if asked), so a following mpt_step sees the
+ * overflow and skips.  The sums' order depends on the list alone: the same
+ * gradients give the same bits. */
+#define MPT_F16 0   /* binary16 */
+#define MPT_BF16 1  /* bfloat16 */
+#define MPT_F32 2   /* binary32 */
+
+#define MPT_LIST_TENSOR_NORMS 0x1u /* also write every tensor's own norm       */
+#define MPT_LIST_UNSCALE 0x2u      /* mpt_list_clip: outputs divided by S      */
+
+typedef struct mpt_list mpt_list;  /* opaque */
+
+/* Bytes of device workspace for a list of n tensors: sizes[n] element counts
+ * (>= 0), types[n] of MPT_F16 / MPT_BF16 / MPT_F32, out_types[n] the types
+ * that mpt_list_clip writes (NULL: the gradients' own).  All host arrays.
+ * Errors: MPT_ERR_INVALID_ARG. */
+int mpt_list_workspace_bytes(const int64_t* sizes, const int32_t* types, const int32_t* out_types,
+                             int32_t n, size_t* bytes);
+
+/* Create a list over a caller-owned device workspace (256-byte aligned, at
+ * least mpt_list_workspace_bytes), synchronously; the workspace must outlive
+ * the list.  Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA. */
+int mpt_list_create(const int64_t* sizes, const int32_t* types, const int32_t* out_types, int32_t n,
+                    void* d_workspace, size_t ws_bytes, mpt_list** out);
+
+/* Queue the norm of the gradients at d_grads (a HOST array of n DEVICE
+ * pointers, as for mpt_step; the pointer of an empty tensor is not looked
+ * at).  S is *d_scale, read on the device when the work runs, or `scale`
+ * where d_scale is NULL (a device S is not checked: it must be finite and
+ * > 0, as mpt_device_scale's always is).  flags: MPT_LIST_TENSOR_NORMS.
+ * The results are written to the workspace (mpt_list_views): result record,
+ * and the tensor norms if asked.  Queues two kernels and returns.
+ * Queue a list's calls on one stream, or order the streams: they share the
+ * workspace.  Pointer tables and CUDA graphs: as for mpt_step_async, with
+ * one difference: a table that a capture has used is kept for good, so four
+ * captured tables leave no room for a fifth table.
+ * Errors: MPT_ERR_INVALID_ARG (also: another device is current; a capture
+ * with a table that no earlier call has used; no table is free),
+ * MPT_ERR_CUDA, MPT_ERR_BROKEN; on an argument error nothing is queued. */
+int mpt_list_norm(mpt_list* h, const void* const* d_grads, float scale, const float* d_scale, float clip,
+                  uint32_t flags, void* cuda_stream);
+
+/* Queue the norm and the scaling of the gradients into d_out (a HOST array of
+ * n DEVICE pointers).  d_out[i] may be d_grads[i] where the types are the
+ * same (in place); apart from that no output may touch a gradient or another
+ * output.  In place and without MPT_LIST_UNSCALE gradients within the limit
+ * are left as they are.  Otherwise as mpt_list_norm.
+ * Errors: as mpt_list_norm, and MPT_ERR_INVALID_ARG for outputs that
+ * overlap. */
+int mpt_list_clip(mpt_list* h, const void* const* d_grads, void* const* d_out, float scale,
+                  const float* d_scale, float clip, uint32_t flags, void* cuda_stream);
+
+/* Device addresses, inside the workspace, of the result record of the last
+ * call and of the n tensor norms.  Either may be NULL.
+ * Errors: MPT_ERR_INVALID_ARG. */
+int mpt_list_views(const mpt_list* h, mpt_check_result** d_result, double** d_tensor_norms);
+
+/* Wait for the work queued on cuda_stream and return the last result (out
+ * may be NULL).  Errors: MPT_ERR_INVALID_ARG, MPT_ERR_CUDA, MPT_ERR_BROKEN. */
+int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out);
+
+/* Release the list's host resources (NULL is accepted). */
+int mpt_list_destroy(mpt_list* h);
+
 #ifdef __cplusplus
 }
 #endif

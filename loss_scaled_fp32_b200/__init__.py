@@ -18,7 +18,7 @@ import os
 
 from . import build as _build
 
-__all__ = ["MPT", "Config", "MptError", "lib", "grad_pointers", "check_flat_noalloc",
+__all__ = ["MPT", "Config", "MptError", "GradList", "lib", "grad_pointers", "check_flat_noalloc",
            "MPT_FLAG_CHECKED", "MPT_FLAG_COUNT_STALE", "MPT_FLAG_GRAD_STATS",
            "MPT_SCALER_DYNAMIC", "MPT_SCALER_DIRECT", "MPT_OPT_MOMENTUM", "MPT_OPT_NESTEROV",
            "MPT_OPT_ADAGRAD"]
@@ -41,6 +41,9 @@ MPT_ERR_BROKEN = -5
 MPT_ERR_TOO_LARGE = -6
 MPT_NOALLOC_MAX_ELEMS = 1 << 30
 MPT_PARTIAL_BYTES = 32
+MPT_F16, MPT_BF16, MPT_F32 = 0, 1, 2
+MPT_LIST_TENSOR_NORMS = 0x1
+MPT_LIST_UNSCALE = 0x2
 
 
 class MptError(RuntimeError):
@@ -134,6 +137,13 @@ def lib():
             "mpt_step_partial": [vp, vp, vp, ctypes.POINTER(vp)],
             "mpt_step_finish": [vp, vp, i32, f32, f32, f32, f32, vp],
             "mpt_debug_fail_next_step": [vp],
+            "mpt_list_workspace_bytes": [vp, vp, vp, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "mpt_list_create": [vp, vp, vp, i32, vp, ctypes.c_size_t, ctypes.POINTER(vp)],
+            "mpt_list_norm": [vp, vp, f32, vp, f32, ctypes.c_uint32, vp],
+            "mpt_list_clip": [vp, vp, vp, f32, vp, f32, ctypes.c_uint32, vp],
+            "mpt_list_views": [vp, ctypes.POINTER(vp), ctypes.POINTER(vp)],
+            "mpt_list_wait": [vp, vp, ctypes.POINTER(CheckResult)],
+            "mpt_list_destroy": [vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -331,6 +341,140 @@ class MPT:
     def close(self):
         if getattr(self, "_h", None):
             lib().mpt_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _type_code(dtype):
+    import torch
+    codes = {torch.float16: MPT_F16, torch.bfloat16: MPT_BF16, torch.float32: MPT_F32}
+    if dtype not in codes:
+        raise ValueError(f"{dtype} is not float16, bfloat16 or float32")
+    return codes[dtype]
+
+
+def _scale_args(scale, device):
+    """(host S, device pointer of S) of a number or a 1-element CUDA tensor."""
+    import torch
+    if isinstance(scale, torch.Tensor):
+        if scale.dtype != torch.float32 or scale.numel() != 1 or scale.device != device:
+            raise ValueError("a scale on the device is one float32 on the same device")
+        return 1.0, ctypes.c_void_p(scale.data_ptr())
+    return float(scale), None
+
+
+class GradList:
+    """Global gradient norm over a fixed list of tensors, and clipping
+    (``mpt_list_*``): FP16, BF16 or FP32 tensors, one type for all or one each.
+
+        clipper = GradList(sizes, torch.bfloat16)
+        clipper.clip(grads, 1.0)            # in place, queued
+        norm = clipper.wait()["grad_norm"]
+
+    ``scale`` is the loss scale S that the gradients carry: a number, or a
+    1-element float32 CUDA tensor such as :meth:`MPT.device_scale`.  The calls
+    return views of the list's own result buffers, which the next call
+    overwrites: ``norm`` (float64), ``coef`` (float32), ``found_inf`` (int32),
+    ``n_nonfinite`` (int64), and ``tensor_norms`` (float64) if asked.
+    """
+
+    def __init__(self, sizes, dtypes, out_dtypes=None, device=None):
+        import torch
+        self.sizes = [int(s) for s in sizes]
+        self.n = len(self.sizes)
+        self.dtypes = self._types(dtypes)
+        self.out_dtypes = self.dtypes if out_dtypes is None else self._types(out_dtypes)
+        self.device = torch.device(device if device is not None else "cuda")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        i32n = ctypes.c_int32 * self.n
+        args = ((ctypes.c_int64 * self.n)(*self.sizes), i32n(*map(_type_code, self.dtypes)),
+                i32n(*map(_type_code, self.out_dtypes)), self.n)
+        nbytes = ctypes.c_size_t()
+        _check(lib().mpt_list_workspace_bytes(*args, ctypes.byref(nbytes)), "mpt_list_workspace_bytes")
+        self.workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=self.device)
+        self._h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(lib().mpt_list_create(*args, ctypes.c_void_p(self.workspace.data_ptr()), nbytes.value,
+                                         ctypes.byref(self._h)), "mpt_list_create")
+        rec, norms = ctypes.c_void_p(), ctypes.c_void_p()
+        _check(lib().mpt_list_views(self._h, ctypes.byref(rec), ctypes.byref(norms)), "mpt_list_views")
+
+        def view(address, nbytes, dtype):
+            off = address - self.workspace.data_ptr()
+            return self.workspace[off:off + nbytes].view(dtype)
+        field = CheckResult
+        self._result = {"norm": view(rec.value + field.grad_norm.offset, 8, torch.float64),
+                        "coef": view(rec.value + field.clip_coef.offset, 4, torch.float32),
+                        "found_inf": view(rec.value + field.found_inf.offset, 4, torch.int32),
+                        "n_nonfinite": view(rec.value + field.n_nonfinite.offset, 8, torch.int64)}
+        self._tensor_norms = view(norms.value, 8 * self.n, torch.float64)
+
+    def _types(self, dtypes):
+        import torch
+        if isinstance(dtypes, torch.dtype):
+            return [dtypes] * self.n
+        dtypes = list(dtypes)
+        if len(dtypes) != self.n:
+            raise ValueError(f"expected {self.n} types, got {len(dtypes)}")
+        return dtypes
+
+    def _ptrs(self, tensors, dtypes, what):
+        if isinstance(tensors, ctypes.Array):
+            if len(tensors) != self.n:
+                raise ValueError(f"expected {self.n} {what} pointers, got {len(tensors)}")
+            return tensors
+        if len(tensors) != self.n:
+            raise ValueError(f"expected {self.n} {what} tensors, got {len(tensors)}")
+        for t, n, dt in zip(tensors, self.sizes, dtypes):
+            if t.numel() != n or t.dtype != dt or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{what} tensor does not match its size/dtype/device or is not contiguous")
+        return grad_pointers(tensors)
+
+    def _views(self, tensor_norms):
+        return self._result | {"tensor_norms": self._tensor_norms} if tensor_norms else dict(self._result)
+
+    def norm(self, grads, scale=1.0, clip=0.0, tensor_norms=False, stream=None):
+        """Queue the norm of ``grads`` (CUDA tensors, or an array from
+        :func:`grad_pointers`); ``clip`` only sets the ``coef`` reported."""
+        import torch
+        host, dev = _scale_args(scale, self.device)
+        with torch.cuda.device(self.device):
+            _check(lib().mpt_list_norm(self._h, self._ptrs(grads, self.dtypes, "gradient"), host, dev, clip,
+                                       MPT_LIST_TENSOR_NORMS if tensor_norms else 0,
+                                       _stream_ptr(stream, self.device)), "mpt_list_norm")
+        return self._views(tensor_norms)
+
+    def clip(self, grads, clip, out=None, scale=1.0, unscale=False, tensor_norms=False, stream=None):
+        """Queue the norm and the scaling of ``grads`` to a norm of at most
+        ``clip``, into ``out`` (default: in place)."""
+        import torch
+        host, dev = _scale_args(scale, self.device)
+        g = self._ptrs(grads, self.dtypes, "gradient")
+        if out is None and self.out_dtypes != self.dtypes:
+            raise ValueError("outputs of another type need tensors of their own")
+        o = g if out is None else self._ptrs(out, self.out_dtypes, "output")
+        flags = (MPT_LIST_TENSOR_NORMS if tensor_norms else 0) | (MPT_LIST_UNSCALE if unscale else 0)
+        with torch.cuda.device(self.device):
+            _check(lib().mpt_list_clip(self._h, g, o, host, dev, clip, flags,
+                                       _stream_ptr(stream, self.device)), "mpt_list_clip")
+        return self._views(tensor_norms)
+
+    def wait(self, stream=None):
+        """Wait for the queued work; the last result as a dict of numbers."""
+        r = CheckResult()
+        _check(lib().mpt_list_wait(self._h, _stream_ptr(stream, self.device), ctypes.byref(r)),
+               "mpt_list_wait")
+        return r.as_dict()
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().mpt_list_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmpt.so")
 STAMP = LIB + ".sha256"
-SOURCES = [os.path.join(CSRC, f) for f in ("mpt.cu", "mpt_kernels.cuh", "mpt_internal.h")] + \
+UNITS = ("mpt.cu", "mpt_list.cu")
+SOURCES = [os.path.join(CSRC, f) for f in UNITS + ("mpt_kernels.cuh", "mpt_internal.h")] + \
     [os.path.join(ROOT, "include", "mpt.h")]
 
 NVCC_FLAGS = [
@@ -74,7 +75,8 @@ def build(force=False, verbose=False):
             if f.read().strip() == digest:
                 return LIB
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, os.path.join(CSRC, "mpt.cu"), "-o", tmp]
+    cmd = [nvcc(), *NVCC_FLAGS, "--threads", str(len(UNITS)),
+           *[os.path.join(CSRC, f) for f in UNITS], "-o", tmp]
     out = subprocess.run(cmd, capture_output=True, text=True)
     if out.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + out.stdout + out.stderr)
