@@ -474,6 +474,71 @@ int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out);
 /* Release the list's host resources (NULL is accepted). */
 int mpt_list_destroy(mpt_list* h);
 
+/* ---- softmax cross entropy of a head, with loss-scaled gradients ---------
+ *
+ * The start of the backward pass: the loss that S multiplies.  For n rows of
+ * hidden (n x d), a head's weight (v x d) and one target class per row,
+ *
+ *   z      = hidden weight^T                    (never stored)
+ *   loss_i = log(sum_u exp(z_iu)) - z_it        (0 where t == ignore_index)
+ *   loss   = sum of loss_i, or that divided by the number of rows that are
+ *            not ignored (MPT_XENT_MEAN; 0 where every row is)
+ *   grad_hidden = S dloss/dhidden,  grad_weight = S dloss/dweight
+ *
+ * FP16 or BF16 operands and gradients of the same type; products are summed
+ * in binary32, exponentials and their sums are binary32, the gradient of the
+ * logits is rounded to 16 bits once (scaled so that it does not underflow),
+ * and S/n is applied in binary32 before the gradients are rounded: a value
+ * beyond FP16's range becomes inf there, which mpt_step finds and skips on.
+ * A target that is neither ignored nor a class makes the loss and the
+ * gradients NaN (and nothing out of range is read).  Each result depends on
+ * the call's arguments alone, bit for bit: no sum's order depends on timing. */
+#define MPT_XENT_MEAN 0
+#define MPT_XENT_SUM 1
+
+typedef struct {
+    int32_t type;             /* MPT_F16 or MPT_BF16                             */
+    int32_t target_bytes;     /* 4 (int32) or 8 (int64, default)                  */
+    int64_t n, v, d;          /* rows (>= 0), classes (>= 1), width (a multiple
+                                 of 8)                                            */
+    const void* hidden;       /* n rows of d, ld_hidden elements apart: 16-byte
+                                 aligned, ld a multiple of 8                      */
+    int64_t ld_hidden;
+    const void* weight;       /* v rows of d, likewise                            */
+    int64_t ld_weight;
+    const void* targets;      /* n integers                                       */
+    int64_t ignore_index;     /* rows with this target do not count (-100)        */
+    int32_t reduction;        /* MPT_XENT_MEAN (default) or MPT_XENT_SUM          */
+    float scale;              /* S (default 1), or                                */
+    const float* d_scale;     /* S on the device, read when the work runs         */
+    float* loss;              /* out: 1 value                                     */
+    float* token_loss;        /* out: n values, or NULL                           */
+    float* lse;               /* out: n values, log sum exp z, or NULL            */
+    int64_t* n_valid;         /* out: rows that are not ignored, or NULL          */
+    void* grad_hidden;        /* out: n rows of d, or NULL                        */
+    int64_t ld_grad_hidden;
+    void* grad_weight;        /* out: v rows of d, or NULL                        */
+    int64_t ld_grad_weight;
+} mpt_xent_args;
+
+/* Fill *args with zeros and the defaults named above.
+ * Errors: MPT_ERR_INVALID_ARG. */
+int mpt_xent_args_init(mpt_xent_args* args);
+
+/* Bytes of device workspace for these sizes and these outputs (which of
+ * grad_hidden and grad_weight are asked for; addresses are not looked at
+ * otherwise).  Errors: MPT_ERR_INVALID_ARG. */
+int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes);
+
+/* Queue the loss and the gradients asked for on cuda_stream and return.  All
+ * pointers are device pointers of the current device; gradients may not touch
+ * hidden, weight or each other.  The workspace (256-byte aligned) holds
+ * nothing between calls: calls that may overlap on the GPU need one each.
+ * Can be captured into a CUDA graph.
+ * Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA; on an
+ * argument error nothing is queued. */
+int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,12 +13,13 @@ cannot be loaded (or built with nvcc), importing the library fails loudly.
     res = opt.step(grads, scale=opt.scale, lr=0.01, momentum=0.9,
                    weight_decay=1e-4, clip=1.0)
 """
+import collections
 import ctypes
 import os
 
 from . import build as _build
 
-__all__ = ["MPT", "Config", "MptError", "GradList", "lib", "grad_pointers", "check_flat_noalloc",
+__all__ = ["MPT", "Config", "MptError", "GradList", "xent_loss", "xent_grad", "lib", "grad_pointers", "check_flat_noalloc",
            "MPT_FLAG_CHECKED", "MPT_FLAG_COUNT_STALE", "MPT_FLAG_GRAD_STATS",
            "MPT_SCALER_DYNAMIC", "MPT_SCALER_DIRECT", "MPT_OPT_MOMENTUM", "MPT_OPT_NESTEROV",
            "MPT_OPT_ADAGRAD"]
@@ -44,6 +45,7 @@ MPT_PARTIAL_BYTES = 32
 MPT_F16, MPT_BF16, MPT_F32 = 0, 1, 2
 MPT_LIST_TENSOR_NORMS = 0x1
 MPT_LIST_UNSCALE = 0x2
+MPT_XENT_MEAN, MPT_XENT_SUM = 0, 1
 
 
 class MptError(RuntimeError):
@@ -89,6 +91,21 @@ class CheckResult(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "reserved"}
+
+
+class XentArgs(ctypes.Structure):
+    """``mpt_xent_args``."""
+    _fields_ = [("type", ctypes.c_int32), ("target_bytes", ctypes.c_int32),
+                ("n", ctypes.c_int64), ("v", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("hidden", ctypes.c_void_p), ("ld_hidden", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("ld_weight", ctypes.c_int64),
+                ("targets", ctypes.c_void_p), ("ignore_index", ctypes.c_int64),
+                ("reduction", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("d_scale", ctypes.c_void_p), ("loss", ctypes.c_void_p),
+                ("token_loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("n_valid", ctypes.c_void_p), ("grad_hidden", ctypes.c_void_p),
+                ("ld_grad_hidden", ctypes.c_int64), ("grad_weight", ctypes.c_void_p),
+                ("ld_grad_weight", ctypes.c_int64)]
 
 
 class Stats(ctypes.Structure):
@@ -144,6 +161,9 @@ def lib():
             "mpt_list_views": [vp, ctypes.POINTER(vp), ctypes.POINTER(vp)],
             "mpt_list_wait": [vp, vp, ctypes.POINTER(CheckResult)],
             "mpt_list_destroy": [vp],
+            "mpt_xent_args_init": [ctypes.POINTER(XentArgs)],
+            "mpt_xent_workspace_bytes": [ctypes.POINTER(XentArgs), ctypes.POINTER(ctypes.c_size_t)],
+            "mpt_xent": [ctypes.POINTER(XentArgs), vp, ctypes.c_size_t, vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -482,3 +502,83 @@ class GradList:
             self.close()
         except Exception:
             pass
+
+
+XentLoss = collections.namedtuple("XentLoss", "loss token_loss lse n_valid")
+XentGrad = collections.namedtuple("XentGrad", "loss token_loss lse n_valid grad_hidden grad_weight")
+
+
+def _rows(t, what, like=None):
+    """The row distance of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a 2-D CUDA tensor with contiguous rows")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must have the type and device of hidden")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, grad_weight, stream):
+    import torch
+    a = XentArgs()
+    lib().mpt_xent_args_init(ctypes.byref(a))
+    a.ld_hidden, a.ld_weight = _rows(hidden, "hidden"), _rows(weight, "weight", hidden)
+    a.type = _type_code(hidden.dtype)
+    a.n, a.d = hidden.shape
+    a.v = weight.shape[0]
+    dev = hidden.device
+    if weight.shape[1] != a.d:
+        raise ValueError("hidden and weight must have rows of one width")
+    if targets.shape != (a.n,) or targets.device != dev or not targets.is_contiguous() or \
+            targets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("targets must be one int32 or int64 per row of hidden, contiguous, on its device")
+    if reduction not in ("mean", "sum"):
+        raise ValueError("reduction is 'mean' or 'sum'")
+    a.target_bytes = targets.element_size()
+    a.ignore_index = ignore_index
+    a.reduction = MPT_XENT_SUM if reduction == "sum" else MPT_XENT_MEAN
+    a.scale, a.d_scale = _scale_args(scale, dev)
+    a.hidden, a.weight, a.targets = hidden.data_ptr(), weight.data_ptr(), targets.data_ptr()
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    # what the call allocates belongs to the stream that it runs on
+    with torch.cuda.device(dev), torch.cuda.stream(s):
+        out = torch.empty(2 * a.n + 4, dtype=torch.float32, device=dev)
+        n_valid = out[:2].view(torch.int64)
+        loss, token_loss, lse = out[2:3], out[4:4 + a.n], out[4 + a.n:]
+        grads = []
+        for given, like, name in ((grad_hidden, hidden, "grad_hidden"), (grad_weight, weight, "grad_weight")):
+            if given is True:
+                given = torch.empty(like.shape, dtype=like.dtype, device=dev)
+            elif given is False or given is None:
+                given = None
+            elif given.shape != like.shape:
+                raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
+            if given is not None:
+                setattr(a, "ld_" + name, _rows(given, name, hidden))
+                setattr(a, name, given.data_ptr())
+            grads.append(given)
+        a.loss, a.token_loss, a.lse, a.n_valid = (t.data_ptr() for t in (loss, token_loss, lse, n_valid))
+        nbytes = ctypes.c_size_t()
+        _check(lib().mpt_xent_workspace_bytes(ctypes.byref(a), ctypes.byref(nbytes)), "mpt_xent_workspace_bytes")
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        _check(lib().mpt_xent(ctypes.byref(a), ctypes.c_void_p(ws.data_ptr()), nbytes.value,
+                              ctypes.c_void_p(s.cuda_stream)), "mpt_xent")
+    return loss, token_loss, lse, n_valid, grads[0], grads[1]
+
+
+def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stream=None):
+    """Softmax cross entropy of ``hidden @ weight.T`` against ``targets``
+    (``mpt_xent`` without gradients), queued; the logits are not stored.
+
+    Returns ``XentLoss``: ``loss`` (float32, 1 value), ``token_loss`` and
+    ``lse`` (float32, one per row), ``n_valid`` (int64, 1 value)."""
+    return XentLoss(*_xent(hidden, weight, targets, 1.0, ignore_index, reduction, None, None, stream)[:4])
+
+
+def xent_grad(hidden, weight, targets, scale=1.0, ignore_index=-100, reduction="mean", grad_hidden=True,
+              grad_weight=True, stream=None):
+    """The same with the gradients of ``scale * loss`` (``mpt_xent``).
+
+    ``scale`` is S: a number, or a 1-element float32 CUDA tensor such as
+    :meth:`MPT.device_scale`.  ``grad_hidden`` and ``grad_weight`` are tensors
+    to write, True for new ones, or None for none.  Returns ``XentGrad``."""
+    return XentGrad(*_xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, grad_weight, stream))

@@ -18,8 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmpt.so")
 STAMP = LIB + ".sha256"
-UNITS = ("mpt.cu", "mpt_list.cu")
-SOURCES = [os.path.join(CSRC, f) for f in UNITS + ("mpt_kernels.cuh", "mpt_internal.h")] + \
+UNITS = ("mpt.cu", "mpt_list.cu", "mpt_xent.cu")
+SOURCES = [os.path.join(CSRC, f) for f in UNITS + ("mpt_kernels.cuh", "mpt_internal.h", "sm100.cuh")] + \
     [os.path.join(ROOT, "include", "mpt.h")]
 
 NVCC_FLAGS = [

@@ -1,0 +1,968 @@
+// mpt_xent.cu -- softmax cross entropy of a linear head over a large
+// vocabulary, with its loss-scaled gradients (mpt_xent of include/mpt.h).
+//
+//   z = H W^T            H: n x d activations, W: v x d head, 16-bit
+//   loss_i = log(1 + sum_{u != t} exp(z_u - z_t)),  t = target of row i
+//   dz_iu  = exp(z_iu - lse_i) - [u = t]            (at u = t: expm1(-loss_i))
+//   dH = g dz W,  dW = g dz^T H,  g = S / valid rows (or S)
+//
+// The logits are never kept.  The forward pass reduces each 256-column tile of
+// z to a maximum and a sum per row while the next tile is multiplied; the
+// backward pass goes through the vocabulary in pieces: multiply z again, write
+// dz of the piece in 16 bits, and multiply it with W (dH, summed over the
+// pieces in binary32) and with H (this piece's rows of dW, final at once).
+//
+// The loss is formed from the other columns' sum against the target's logit,
+// so a sure answer's small loss keeps its digits, and dz at the target comes
+// from the loss for the same reason.  dz is rounded to 16 bits once, scaled
+// by 2^15 in binary16 so that probabilities down to 2^-29 keep full
+// precision; the loss scale and 1/n are applied to the binary32 sums.
+//
+// All four products run on the tensor cores in one kernel: one CTA per SM,
+// one warp that loads tiles by TMA, one thread that issues the products, four
+// warps that turn finished accumulators into results; two accumulators in
+// tensor memory let the products of a tile run under the results of the last.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "../../include/mpt.h"
+#include "sm100.cuh"
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kStages = 4;
+constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kThreads = 256;           // warps 0-3: load, multiply, tensor memory, idle; 4-7: results
+constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kMaxCtas = 148;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr size_t kAlign = 256;
+
+enum Mode { kLoss, kDz, kGrad };
+
+// One product: mt x nt output tiles, each summed over kb blocks of 64, the
+// sum cut into `splits` parts.
+struct Job {
+    int32_t mt, nt, splits, kb;
+    int32_t a_mn, b_mn;   // operand major-ness
+    uint32_t idesc;
+    int32_t tiles;
+};
+
+struct RowStats {
+    const float* lse;
+    const float* loss;
+};
+
+struct GemmArgs {
+    CUtensorMap a[2], b[2];
+    Job job[2];           // kGrad: dH, then dW
+    int32_t tiles;
+    // rows and columns of the logits
+    int32_t n, v;
+    const void* targets;
+    int32_t target_bytes;
+    int64_t ignore;
+    // kLoss
+    float2* part;         // [n][part_ld]: maximum and sum of a tile's row
+    float* zt;            // [n]: the target's logit
+    int32_t part_ld;
+    int32_t* status;      // one per CTA: 1 after a wait that ran out
+    // kDz
+    RowStats stats;
+    uint16_t* dz;         // [n][dz_ld], columns col0 ...
+    int64_t dz_ld;
+    int32_t col0;
+    float exponent;       // dz is scaled by 2^exponent
+    // kGrad
+    float* dh;            // [splits][n][d] binary32 sums over the pieces
+    int32_t d;
+    int32_t add;          // add to what an earlier piece left there
+    uint16_t* dw;         // rows of this piece
+    int64_t dw_ld;
+    int32_t dw_rows;
+    int32_t dw_wide;      // 16-byte stores are aligned
+    const float* gscale;
+    float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
+};
+
+__device__ __forceinline__ int64_t target_of(const GemmArgs& g, int row)
+{
+    return g.target_bytes == 8 ? static_cast<const int64_t*>(g.targets)[row]
+                               : (int64_t)static_cast<const int32_t*>(g.targets)[row];
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float x, float y)
+{
+    if constexpr (kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+struct Tile {
+    int job, m, n, split, kb0, kb1;
+};
+
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t)
+{
+    Tile r;
+    r.job = t >= g.job[0].tiles ? 1 : 0;
+    const Job& j = g.job[r.job];
+    int i = t - (r.job ? g.job[0].tiles : 0);
+    r.m = i % j.mt;
+    i /= j.mt;
+    r.n = i % j.nt;
+    r.split = i / j.nt;
+    r.kb0 = (int)((int64_t)j.kb * r.split / j.splits);
+    r.kb1 = (int)((int64_t)j.kb * (r.split + 1) / j.splits);
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// results: one thread per row of the tile, 32 columns at a time
+// ---------------------------------------------------------------------------
+
+// Maximum and sum of exponentials of 256 columns; the target's column is left
+// out of the sum and its logit kept.
+__device__ __forceinline__ void rows_loss(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+{
+    const int col0 = t.n * kTileN;
+    const int64_t target = row < g.n ? target_of(g, row) : -1;
+    const int cols = min(kTileN, g.v - col0);
+    const int64_t hit64 = target - col0;
+    const int hit = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < kTileN ? (int)hit64 : -1;
+    float top = -INFINITY, sum = 0.0f, zt = 0.0f;
+    uint32_t r[32];
+#pragma unroll 1
+    for (int c = 0; c < kTileN; c += 32) {
+        if (c >= cols)
+            break;
+        __syncwarp();
+        tmem_load32(tmem + c, r);
+        tmem_wait_load(r);
+        float* z = reinterpret_cast<float*>(r);
+        if (c + 32 > cols) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                z[k] = c + k < cols ? z[k] : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, hit >= c && hit < c + 32)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const bool here = c + k == hit;
+                zt = here ? z[k] : zt;
+                z[k] = here ? -INFINITY : z[k];
+            }
+        }
+        float m4[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int k = 4; k < 32; ++k)
+            m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+        const float now = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), top);
+        // a row of nothing but -inf sums to zero: no inf - inf
+        const float base = now == -INFINITY ? 0.0f : now * kLog2e;
+        float s4[4] = {sum * exp2_fast(fmaf(top, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
+        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        top = now;
+    }
+    if (row < g.n) {
+        g.part[(int64_t)row * g.part_ld + t.n] = make_float2(top, sum);
+        if (hit >= 0)
+            g.zt[row] = zt;
+    }
+}
+
+// dz of 256 columns, rounded to 16 bits once.
+template <bool kBf16>
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+{
+    const int col0 = t.n * kTileN;               // inside the piece
+    const int cols = min(kTileN, g.v - g.col0 - col0);
+    float base = 0.0f, at_target = 0.0f;
+    int hit = -1;
+    bool live = false;
+    if (row < g.n) {
+        const int64_t target = target_of(g, row);
+        live = target != g.ignore;
+        base = fmaf(-g.stats.lse[row], kLog2e, g.exponent);
+        at_target = ldexpf(expm1f(-g.stats.loss[row]), (int)g.exponent);
+        const int64_t h = target - g.col0 - col0;
+        hit = live && target >= 0 && target < g.v && h >= 0 && h < kTileN ? (int)h : -1;
+    }
+    uint16_t* out = g.dz + (int64_t)row * g.dz_ld + col0;
+    uint32_t r[32];
+#pragma unroll 1
+    for (int c = 0; c < kTileN; c += 32) {
+        __syncwarp();
+        tmem_load32(tmem + c, r);
+        tmem_wait_load(r);
+        float* z = reinterpret_cast<float*>(r);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            z[k] = exp2_fast(fmaf(z[k], kLog2e, base));
+        if (c + 32 > cols || !live) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                z[k] = live && c + k < cols ? z[k] : 0.0f;
+        }
+        if (hit >= c && hit < c + 32) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                z[k] = c + k == hit ? at_target : z[k];
+        }
+        if (row < g.n) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint4 o;
+                o.x = pack2<kBf16>(z[8 * k], z[8 * k + 1]);
+                o.y = pack2<kBf16>(z[8 * k + 2], z[8 * k + 3]);
+                o.z = pack2<kBf16>(z[8 * k + 4], z[8 * k + 5]);
+                o.w = pack2<kBf16>(z[8 * k + 6], z[8 * k + 7]);
+                *reinterpret_cast<uint4*>(out + c + 8 * k) = o;
+            }
+        }
+    }
+}
+
+// 256 columns of dH's binary32 sums (d is a multiple of 8).
+__device__ __forceinline__ void rows_dh(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+{
+    const int col0 = t.n * kTileN;
+    float* out = g.dh + ((int64_t)t.split * g.n + row) * g.d + col0;
+    uint32_t r[32];
+#pragma unroll 1
+    for (int c = 0; c < kTileN; c += 32) {
+        if (col0 + c >= g.d)
+            break;
+        __syncwarp();
+        tmem_load32(tmem + c, r);
+        tmem_wait_load(r);
+        const float* z = reinterpret_cast<const float*>(r);
+        if (row < g.n) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                if (col0 + c + k < g.d) {
+                    float4 o = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
+                    float4* to = reinterpret_cast<float4*>(out + c + k);
+                    if (g.add) {
+                        const float4 old = *to;
+                        o.x += old.x;
+                        o.y += old.y;
+                        o.z += old.z;
+                        o.w += old.w;
+                    }
+                    *to = o;
+                }
+            }
+        }
+    }
+}
+
+// 256 columns of dW, final.
+template <bool kBf16>
+__device__ __forceinline__ void rows_dw(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+{
+    const int col0 = t.n * kTileN;
+    const float scale = *g.gscale;
+    uint16_t* out = g.dw + (int64_t)row * g.dw_ld + col0;
+    uint32_t r[32];
+#pragma unroll 1
+    for (int c = 0; c < kTileN; c += 32) {
+        if (col0 + c >= g.d)
+            break;
+        __syncwarp();
+        tmem_load32(tmem + c, r);
+        tmem_wait_load(r);
+        const float* z = reinterpret_cast<const float*>(r);
+        if (row < g.dw_rows) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                if (col0 + c + k < g.d) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = pack2<kBf16>(z[k + 2 * e] * scale, z[k + 2 * e + 1] * scale);
+                    if (g.dw_wide) {
+                        *reinterpret_cast<uint4*>(out + c + k) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            out[c + k + 2 * e] = (uint16_t)(o[e] & 0xFFFFu);
+                            out[c + k + 2 * e + 1] = (uint16_t)(o[e] >> 16);
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product kernel
+// ---------------------------------------------------------------------------
+
+template <int kMode, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
+{
+    extern __shared__ uint8_t dyn[];
+    __shared__ alignas(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_dead;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tiles_at = (smem_addr(dyn) + 1023u) & ~1023u;  // swizzle atoms are 1024 bytes
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_addr(&s_full[s]), 1);
+            mbar_init(smem_addr(&s_empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&s_acc_full[b]), 1);
+            mbar_init(smem_addr(&s_acc_empty[b]), 4);
+        }
+        mbar_init(smem_addr(&s_drain), 1);
+        s_dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 2)
+        tmem_alloc(smem_addr(&s_tmem), 512);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    volatile int* dead = &s_dead;
+
+    if (warp == 0 && lane == 0) {
+        // ---- loads
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+            const Tile u = tile_at(g, t);
+            const Job& j = g.job[u.job];
+            const CUtensorMap* ma = &g.a[u.job];
+            const CUtensorMap* mb = &g.b[u.job];
+            for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+                const uint32_t s = it % kStages, phase = (it / kStages) & 1;
+                if (!(ok = mbar_wait(smem_addr(&s_empty[s]), phase ^ 1, dead)))
+                    break;
+                const uint32_t full = smem_addr(&s_full[s]);
+                const uint32_t at_a = tiles_at + s * kStageBytes, at_b = at_a + kBytesA;
+                mbar_expect(full, kStageBytes);
+                if (j.a_mn) {
+                    for (int q = 0; q < kTileM / 64; ++q)
+                        tma_load(at_a + q * (64 * kTileK * 2), ma, full, u.m * kTileM + q * 64, kb * kTileK);
+                } else {
+                    tma_load(at_a, ma, full, kb * kTileK, u.m * kTileM);
+                }
+                if (j.b_mn) {
+                    for (int q = 0; q < kTileN / 64; ++q)
+                        tma_load(at_b + q * (64 * kTileK * 2), mb, full, u.n * kTileN + q * 64, kb * kTileK);
+                } else {
+                    tma_load(at_b, mb, full, kb * kTileK, u.n * kTileN);
+                }
+            }
+        }
+        if (!ok) {  // let the loads in flight land before the block leaves
+            for (uint32_t b = it > kStages ? it - kStages : 0; b < it; ++b)
+                mbar_wait(smem_addr(&s_full[b % kStages]), (b / kStages) & 1, nullptr);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- products
+        uint32_t it = 0, acc = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x, ++acc) {
+            const Tile u = tile_at(g, t);
+            const Job& j = g.job[u.job];
+            const uint32_t buf = acc & 1;
+            if (!(ok = mbar_wait(smem_addr(&s_acc_empty[buf]), ((acc >> 1) & 1) ^ 1, dead)))
+                break;
+            fence_after_sync();
+            const uint32_t d = tmem + buf * kTileN;
+            // one product takes 16 of K: 32 bytes along a row, or 16 rows
+            const uint32_t step_a = j.a_mn ? 2048 : 32, step_b = j.b_mn ? 2048 : 32;
+            const uint32_t block = 64 * kTileK * 2;
+            for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+                const uint32_t s = it % kStages;
+                if (!(ok = mbar_wait(smem_addr(&s_full[s]), (it / kStages) & 1, dead)))
+                    break;
+                fence_after_sync();
+                const uint32_t at_a = tiles_at + s * kStageBytes, at_b = at_a + kBytesA;
+#pragma unroll
+                for (int k = 0; k < kTileK / 16; ++k)
+                    mma_f16(d, smem_desc(at_a + k * step_a, block, 1024), smem_desc(at_b + k * step_b, block, 1024),
+                            j.idesc, kb > u.kb0 || k > 0);
+                mma_commit(smem_addr(&s_empty[s]));
+            }
+            if (ok)
+                mma_commit(smem_addr(&s_acc_full[buf]));
+        }
+        if (!ok) {  // let the products in flight end before tensor memory is freed
+            mma_commit(smem_addr(&s_drain));
+            mbar_wait(smem_addr(&s_drain), 0, nullptr);
+        }
+    } else if (warp >= 4) {
+        // ---- results
+        const int quad = warp & 3;  // a warp reads the 32 lanes of its quarter
+        uint32_t acc = 0;
+        for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++acc) {
+            const Tile u = tile_at(g, t);
+            const uint32_t buf = acc & 1;
+            const int row = u.m * kTileM + quad * 32 + lane;
+            const bool ok = mbar_wait(smem_addr(&s_acc_full[buf]), (acc >> 1) & 1, dead);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            fence_after_sync();
+            const uint32_t at = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
+            if constexpr (kMode == kLoss) {
+                rows_loss(g, u, at, row);
+            } else if constexpr (kMode == kDz) {
+                rows_dz<kBf16>(g, u, at, row);
+            } else {
+                if (u.job == 0)
+                    rows_dh(g, u, at, row);
+                else
+                    rows_dw<kBf16>(g, u, at, row);
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&s_acc_empty[buf]));
+        }
+    }
+    __syncwarp();
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == 2)
+        tmem_free(tmem, 512);
+    if (threadIdx.x == 0) {
+        if constexpr (kMode == kLoss)
+            g.status[blockIdx.x] = s_dead;
+        else if (s_dead)
+            *g.poison = __int_as_float(0x7fc00000);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// row losses, the mean, and dH
+// ---------------------------------------------------------------------------
+
+struct MergePart {
+    double loss;
+    unsigned long long valid;
+};
+
+constexpr int kMergeRows = 8;  // rows (warps) per CTA
+
+__global__ void __launch_bounds__(kMergeRows * 32)
+xent_merge_kernel(GemmArgs g, float* token_loss, float* lse, MergePart* out)
+{
+    __shared__ float s_loss[kMergeRows];
+    __shared__ int s_valid[kMergeRows];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int row = blockIdx.x * kMergeRows + w;
+    float loss = 0.0f;
+    bool valid = false;
+    if (row < g.n) {
+        const float2* p = g.part + (int64_t)row * g.part_ld;
+        float top = -INFINITY;
+        for (int k = lane; k < g.part_ld; k += 32)
+            top = fmaxf(top, p[k].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        for (int k = lane; k < g.part_ld; k += 32)
+            sum += p[k].y * expf(p[k].x - base);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float others = base + logf(sum);  // -inf where there are none
+        const int64_t t = target_of(g, row);
+        float total = others;
+        valid = t != g.ignore;
+        if (valid) {
+            if (t >= 0 && t < g.v) {
+                const float zt = g.zt[row];
+                const float over = others - zt;
+                loss = fmaxf(over, 0.0f) + log1pf(expf(-fabsf(over)));
+                if (isnan(over))
+                    loss = over;  // fmaxf drops a NaN
+                total = zt + loss;
+            } else {
+                loss = total = __int_as_float(0x7fc00000);  // no such class
+            }
+        }
+        if (lane == 0) {
+            token_loss[row] = loss;
+            lse[row] = total;
+        }
+    }
+    if (lane == 0) {
+        s_loss[w] = loss;
+        s_valid[w] = valid ? 1 : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        MergePart m{0.0, 0};
+        for (int k = 0; k < kMergeRows; ++k) {
+            m.loss += (double)s_loss[k];
+            m.valid += (unsigned long long)s_valid[k];
+        }
+        out[blockIdx.x] = m;
+    }
+}
+
+struct FinalArgs {
+    const MergePart* parts;
+    int32_t nparts;
+    const int32_t* status;
+    int32_t nstatus;
+    int32_t mean;
+    float scale;
+    const float* d_scale;
+    int32_t exponent;
+    float* loss;
+    int64_t* n_valid;
+    float* gscale;
+};
+
+__global__ void __launch_bounds__(256) xent_final_kernel(FinalArgs a)
+{
+    __shared__ double s_loss[8];
+    __shared__ unsigned long long s_valid[8];
+    __shared__ int s_bad;
+    if (threadIdx.x == 0)
+        s_bad = 0;
+    __syncthreads();
+    double loss = 0.0;
+    unsigned long long valid = 0;
+    for (int k = threadIdx.x; k < a.nparts; k += 256) {
+        loss += a.parts[k].loss;
+        valid += a.parts[k].valid;
+    }
+    for (int k = threadIdx.x; k < a.nstatus; k += 256)
+        if (a.status[k])
+            s_bad = 1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        loss += __shfl_xor_sync(0xffffffffu, loss, o);
+        valid += __shfl_xor_sync(0xffffffffu, valid, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        s_loss[threadIdx.x >> 5] = loss;
+        s_valid[threadIdx.x >> 5] = valid;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        loss = 0.0;
+        valid = 0;
+        for (int w = 0; w < 8; ++w) {
+            loss += s_loss[w];
+            valid += s_valid[w];
+        }
+        const double by = a.mean && valid > 0 ? (double)valid : 1.0;
+        *a.loss = s_bad ? __int_as_float(0x7fc00000) : (float)(loss / by);
+        if (a.n_valid)
+            *a.n_valid = (int64_t)valid;
+        const double S = (double)(a.d_scale ? *a.d_scale : a.scale);
+        *a.gscale = (float)ldexp(S / by, -a.exponent);
+    }
+}
+
+// dH = T(g * the sum of the splits), eight columns to a thread.
+template <bool kBf16>
+__global__ void __launch_bounds__(256)
+xent_dh_kernel(const float* part, int32_t splits, int64_t n, int32_t d, const float* gscale, uint16_t* out,
+               int64_t ld, int32_t wide)
+{
+    const int32_t per = d / 8;
+    const float scale = *gscale;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per;
+        const int32_t c = (int32_t)(i % per) * 8;
+        float x[8] = {};
+        for (int s = 0; s < splits; ++s) {
+            const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)s * n + row) * d + c);
+            const float4 lo = p[0], hi = p[1];
+            x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+            x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = pack2<kBf16>(x[2 * e] * scale, x[2 * e + 1] * scale);
+        uint16_t* to = out + row * ld + c;
+        if (wide) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                to[2 * e] = (uint16_t)(o[e] & 0xFFFFu);
+                to[2 * e + 1] = (uint16_t)(o[e] >> 16);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+struct NvtxRange {
+    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+    NvtxRange(const NvtxRange&) = delete;
+    NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+struct Plan {
+    bool grad = false, want_dh = false, want_dw = false;
+    int64_t vtiles = 0;     // 256-column tiles of the whole vocabulary
+    int64_t piece = 0;      // columns of one piece of the backward pass
+    int64_t splits = 1;     // of dH's sums over a piece
+    int64_t merges = 0;
+    size_t off_part = 0, off_zt = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
+           off_dh = 0, total = 0;
+};
+
+// The piece: dz of one piece is at most 256 MB (and at least 2048 columns).
+constexpr int64_t kPieceBytes = 256ll << 20;
+
+int make_plan(const mpt_xent_args& a, Plan& p)
+{
+    p.want_dh = a.grad_hidden != nullptr;
+    p.want_dw = a.grad_weight != nullptr;
+    p.grad = p.want_dh || p.want_dw;
+    p.vtiles = ceil_div(a.v, kTileN);
+    p.merges = ceil_div(a.n, kMergeRows);
+    size_t at = 0;
+    auto region = [&](size_t bytes) {
+        const size_t here = at;
+        at = (size_t)round_up((int64_t)(at + bytes), kAlign);
+        return here;
+    };
+    p.off_ctl = region(256 + sizeof(int32_t) * kMaxCtas);
+    p.off_part = region(sizeof(float2) * (size_t)(a.n * p.vtiles));
+    p.off_zt = region(sizeof(float) * (size_t)a.n);
+    p.off_token = region(sizeof(float) * (size_t)a.n);
+    p.off_lse = region(sizeof(float) * (size_t)a.n);
+    p.off_merge = region(sizeof(MergePart) * (size_t)p.merges);
+    if (p.grad && a.n > 0) {
+        const int64_t fit = std::max<int64_t>(2048, kPieceBytes / (2 * a.n) / kTileN * kTileN);
+        p.piece = std::min(round_up(a.v, kTileN), fit);
+        p.off_dz = region((size_t)(a.n * p.piece * 2));
+        if (p.want_dh) {
+            // cut dH's sums so that one tile is at most half a CTA's share of the piece's work
+            const int64_t kb_v = ceil_div(p.piece, kTileK), kb_n = ceil_div(a.n, kTileK);
+            const int64_t tiles_h = ceil_div(a.n, kTileM) * ceil_div(a.d, kTileN);
+            const int64_t tiles_w = p.want_dw ? ceil_div(p.piece, kTileM) * ceil_div(a.d, kTileN) : 0;
+            const int64_t share = (tiles_h * kb_v + tiles_w * kb_n) / kMaxCtas;
+            p.splits = std::min<int64_t>(64, ceil_div(kb_v, std::max<int64_t>(8, share / 2)));
+            p.off_dh = region((size_t)(p.splits * a.n * a.d * 4));
+        }
+    }
+    p.total = at;
+    return MPT_OK;
+}
+
+bool args_ok(const mpt_xent_args* a)
+{
+    if (!a || (a->type != MPT_F16 && a->type != MPT_BF16))
+        return false;
+    if (a->n < 0 || a->n > (1 << 24) || a->v < 1 || a->v > (1 << 24) || a->d < 8 || a->d > (1 << 20) || a->d % 8 != 0)
+        return false;
+    if (a->target_bytes != 4 && a->target_bytes != 8)
+        return false;
+    if (a->reduction != MPT_XENT_MEAN && a->reduction != MPT_XENT_SUM)
+        return false;
+    // tiles are counted in 31 bits
+    const int64_t most = (int64_t)1 << 30, rows = ceil_div(a->n, kTileM), wide = ceil_div(a->d, kTileN);
+    return rows * ceil_div(a->v, kTileN) <= most && rows * wide * 64 <= most && ceil_div(a->v, kTileM) * wide <= most;
+}
+
+// [lo, hi) of rows of d 16-bit values ld apart
+struct Span {
+    uintptr_t lo, hi;
+};
+Span rows_span(const void* p, int64_t rows, int64_t ld, int64_t d)
+{
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return {lo, rows ? lo + (uintptr_t)((rows - 1) * ld + d) * 2 : lo};
+}
+bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool pointers_ok(const mpt_xent_args& a)
+{
+    const int64_t big = (int64_t)1 << 40;
+    auto rows = [&](const void* p, int64_t ld, uintptr_t align, int64_t quantum) {
+        return p && reinterpret_cast<uintptr_t>(p) % align == 0 && ld >= a.d && ld < big && ld % quantum == 0;
+    };
+    if (!rows(a.weight, a.ld_weight, 16, 8) || !a.loss || (reinterpret_cast<uintptr_t>(a.loss) & 3))
+        return false;
+    if (a.n > 0 && (!rows(a.hidden, a.ld_hidden, 16, 8) || !a.targets ||
+                    reinterpret_cast<uintptr_t>(a.targets) % (uintptr_t)a.target_bytes))
+        return false;
+    if ((reinterpret_cast<uintptr_t>(a.token_loss) & 3) || (reinterpret_cast<uintptr_t>(a.lse) & 3) ||
+        (reinterpret_cast<uintptr_t>(a.n_valid) & 7) || (reinterpret_cast<uintptr_t>(a.d_scale) & 3))
+        return false;
+    if (a.grad_hidden && !rows(a.grad_hidden, a.ld_grad_hidden, 2, 1))
+        return false;
+    if (a.grad_weight && !rows(a.grad_weight, a.ld_grad_weight, 2, 1))
+        return false;
+    // gradients are written while the inputs are still read
+    const Span h = rows_span(a.hidden, a.n, a.ld_hidden, a.d), w = rows_span(a.weight, a.v, a.ld_weight, a.d);
+    const Span gh = a.grad_hidden ? rows_span(a.grad_hidden, a.n, a.ld_grad_hidden, a.d) : Span{0, 0};
+    const Span gw = a.grad_weight ? rows_span(a.grad_weight, a.v, a.ld_grad_weight, a.d) : Span{0, 0};
+    return !(meet(h, gh) || meet(h, gw) || meet(w, gh) || meet(w, gw) || meet(gh, gw));
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+std::atomic<void*> g_encode{nullptr};
+
+EncodeFn encode_fn()
+{
+    void* f = g_encode.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        g_encode.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// A row-major matrix of 16-bit values, cut into boxes of 64 columns; what lies
+// outside reads as zero.
+bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    EncodeFn f = encode_fn();
+    if (!f)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kMode, bool kBf16>
+cudaError_t launch_product(const GemmArgs& g, cudaStream_t st)
+{
+    cudaError_t e = cudaFuncSetAttribute(xent_product_kernel<kMode, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)std::min(g.tiles, kMaxCtas));
+    lc.blockDim = dim3(kThreads);
+    lc.dynamicSmemBytes = kSmem;
+    lc.stream = st;
+    return cudaLaunchKernelEx(&lc, xent_product_kernel<kMode, kBf16>, g);
+}
+
+void set_job(Job& j, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn)
+{
+    j.mt = (int32_t)ceil_div(m, kTileM);
+    j.nt = (int32_t)ceil_div(n, kTileN);
+    j.kb = (int32_t)ceil_div(k, kTileK);
+    j.splits = (int32_t)std::min<int64_t>(splits, j.kb);
+    j.a_mn = a_mn;
+    j.b_mn = b_mn;
+    j.idesc = mma_desc(bf16, a_mn, b_mn, kTileM, kTileN);
+    j.tiles = j.mt * j.nt * j.splits;
+}
+
+template <bool kBf16>
+int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
+{
+    float* gscale = reinterpret_cast<float*>(ws + p.off_ctl);
+    int32_t* status = reinterpret_cast<int32_t*>(ws + p.off_ctl + 256);
+    float* token = a.token_loss ? a.token_loss : reinterpret_cast<float*>(ws + p.off_token);
+    float* lse = a.lse ? a.lse : reinterpret_cast<float*>(ws + p.off_lse);
+    const int exponent = kBf16 ? 0 : 15;
+
+    GemmArgs g{};
+    g.n = (int32_t)a.n;
+    g.v = (int32_t)a.v;
+    g.d = (int32_t)a.d;
+    g.targets = a.targets;
+    g.target_bytes = a.target_bytes;
+    g.ignore = a.ignore_index;
+    g.part = reinterpret_cast<float2*>(ws + p.off_part);
+    g.zt = reinterpret_cast<float*>(ws + p.off_zt);
+    g.part_ld = (int32_t)p.vtiles;
+    g.status = status;
+    g.stats = {lse, token};
+    g.exponent = (float)exponent;
+    g.gscale = gscale;
+    g.poison = a.loss;
+
+    FinalArgs f{};
+    f.mean = a.reduction == MPT_XENT_MEAN;
+    f.scale = a.scale;
+    f.d_scale = a.d_scale;
+    f.exponent = exponent;
+    f.loss = a.loss;
+    f.n_valid = a.n_valid;
+    f.gscale = gscale;
+    f.status = status;
+    f.parts = reinterpret_cast<MergePart*>(ws + p.off_merge);
+
+    if (a.n > 0) {
+        set_job(g.job[0], kBf16, a.n, a.v, a.d, 1, false, false);
+        g.tiles = g.job[0].tiles;
+        if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileM) ||
+            !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, kTileN))
+            return MPT_ERR_CUDA;
+        if (launch_product<kLoss, kBf16>(g, st) != cudaSuccess)
+            return MPT_ERR_CUDA;
+        f.nstatus = std::min(g.tiles, kMaxCtas);
+        xent_merge_kernel<<<(unsigned)p.merges, kMergeRows * 32, 0, st>>>(g, token, lse, const_cast<MergePart*>(f.parts));
+        f.nparts = (int32_t)p.merges;
+    }
+    xent_final_kernel<<<1, 256, 0, st>>>(f);
+    if (cudaGetLastError() != cudaSuccess)
+        return MPT_ERR_CUDA;
+    if (!p.grad)
+        return MPT_OK;
+    if (a.n == 0) {
+        if (p.want_dw && cudaMemset2DAsync(a.grad_weight, (size_t)a.ld_grad_weight * 2, 0, (size_t)a.d * 2,
+                                           (size_t)a.v, st) != cudaSuccess)
+            return MPT_ERR_CUDA;
+        return MPT_OK;
+    }
+
+    uint16_t* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
+    auto wide = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
+    GemmArgs z = g;
+    z.dz = dz;
+    z.dz_ld = p.piece;
+    GemmArgs q = g;
+    q.dh = reinterpret_cast<float*>(ws + p.off_dh);
+    q.dw_ld = a.ld_grad_weight;
+    q.dw_wide = wide(a.grad_weight, a.ld_grad_weight);
+    const uint16_t* w = static_cast<const uint16_t*>(a.weight);
+    int32_t splits = 1;
+    for (int64_t c0 = 0; c0 < a.v; c0 += p.piece) {
+        const int64_t cols = std::min(p.piece, a.v - c0);
+        const uint16_t* wp = w + c0 * a.ld_weight;
+        z.col0 = (int32_t)c0;
+        set_job(z.job[0], kBf16, a.n, cols, a.d, 1, false, false);
+        z.tiles = z.job[0].tiles;
+        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kTileN))
+            return MPT_ERR_CUDA;
+        if (launch_product<kDz, kBf16>(z, st) != cudaSuccess)
+            return MPT_ERR_CUDA;
+
+        // columns beyond `cols` up to the tile's end are zeros in dz
+        q.job[0] = q.job[1] = Job{};
+        if (p.want_dh) {
+            set_job(q.job[0], kBf16, a.n, a.d, cols, p.splits, false, true);
+            // (a short last piece may add to the first sums only)
+            splits = std::max(splits, q.job[0].splits);
+            if (!make_map(&q.a[0], kBf16, dz, a.n, cols, p.piece, kTileM) ||
+                !make_map(&q.b[0], kBf16, wp, cols, a.d, a.ld_weight, kTileK))
+                return MPT_ERR_CUDA;
+            q.add = c0 > 0;
+        }
+        if (p.want_dw) {
+            set_job(q.job[1], kBf16, cols, a.d, a.n, 1, true, true);
+            if (!make_map(&q.a[1], kBf16, dz, a.n, cols, p.piece, kTileK) ||
+                !make_map(&q.b[1], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK))
+                return MPT_ERR_CUDA;
+            q.dw = static_cast<uint16_t*>(a.grad_weight) + c0 * a.ld_grad_weight;
+            q.dw_rows = (int32_t)cols;
+        }
+        q.tiles = q.job[0].tiles + q.job[1].tiles;
+        if (launch_product<kGrad, kBf16>(q, st) != cudaSuccess)
+            return MPT_ERR_CUDA;
+    }
+    if (p.want_dh) {
+        const int64_t blocks = std::min<int64_t>(ceil_div(a.n * (a.d / 8), 256), 148 * 8);
+        xent_dh_kernel<kBf16><<<(unsigned)blocks, 256, 0, st>>>(q.dh, splits, a.n, (int32_t)a.d, gscale,
+                                                                static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden,
+                                                                wide(a.grad_hidden, a.ld_grad_hidden));
+        if (cudaGetLastError() != cudaSuccess)
+            return MPT_ERR_CUDA;
+    }
+    return MPT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mpt_xent_args_init(mpt_xent_args* args)
+{
+    if (!args)
+        return MPT_ERR_INVALID_ARG;
+    std::memset(args, 0, sizeof *args);
+    args->type = MPT_F16;
+    args->target_bytes = 8;
+    args->ignore_index = -100;
+    args->reduction = MPT_XENT_MEAN;
+    args->scale = 1.0f;
+    return MPT_OK;
+}
+
+int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes)
+{
+    if (!args_ok(args) || !bytes)
+        return MPT_ERR_INVALID_ARG;
+    Plan p;
+    const int rc = make_plan(*args, p);
+    if (rc == MPT_OK)
+        *bytes = p.total;
+    return rc;
+}
+
+int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void* cuda_stream)
+{
+    NvtxRange range("mpt.xent");
+    if (!args_ok(args) || !pointers_ok(*args))
+        return MPT_ERR_INVALID_ARG;
+    if (!args->d_scale && (!std::isfinite(args->scale) || !(args->scale > 0.0f)))
+        return MPT_ERR_INVALID_ARG;
+    Plan p;
+    const int rc = make_plan(*args, p);
+    if (rc != MPT_OK)
+        return rc;
+    if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % kAlign != 0 || ws_bytes < p.total)
+        return MPT_ERR_WORKSPACE;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    char* ws = static_cast<char*>(d_workspace);
+    const int done = args->type == MPT_BF16 ? enqueue<true>(*args, p, ws, st) : enqueue<false>(*args, p, ws, st);
+    if (done != MPT_OK)
+        cudaGetLastError();  // this call's own error
+    return done;
+}
+
+}  // extern "C"
