@@ -19,9 +19,12 @@
 // precision; the loss scale and 1/n are applied to the binary32 sums.
 //
 // All four products run on the tensor cores in one kernel: one CTA per SM,
-// one warp that loads tiles by TMA, one thread that issues the products, four
+// one thread that loads tiles by TMA, one that issues the products, eight
 // warps that turn finished accumulators into results; two accumulators in
 // tensor memory let the products of a tile run under the results of the last.
+// Two CTAs share a tile of 256 x 256 (each loads half of either operand, so
+// an operand byte feeds twice the products); for at most 128 rows every CTA
+// works alone on 128 x 256.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,12 +42,27 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kStages = 4;
-constexpr int kBytesA = kTileM * kTileK * 2, kBytesB = kTileN * kTileK * 2;
-constexpr int kStageBytes = kBytesA + kBytesB;
-constexpr int kThreads = 256;           // warps 0-3: load, multiply, tensor memory, idle; 4-7: results
-constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kRows = 128;              // of a CTA's tile
+constexpr int kTileN = 256, kTileK = 64;
+constexpr int kResultWarps = 8, kThreads = 32 * (kResultWarps + 2);  // then one that loads, one that multiplies
+constexpr int kBytesA = kRows * kTileK * 2;
+constexpr int kHalf = kTileN / 2;       // columns of one result warp
+// The tensor cores drop what lies below an accumulator's last place, 16 of K
+// at a time: over 2048 of K that adds up to 2e-6 of a large logit.  The
+// forward pass therefore takes its sums out after 512 of K and adds them with
+// rounding to nearest (5e-7); the backward pass, whose results are rounded to
+// 16 bits, need not.
+constexpr int kPromote = 512 / kTileK;
+
+// Shared memory of one load stage, and how many fit.
+template <bool kPair> struct Shape {
+    static constexpr int kBytesB = (kPair ? kTileN / 2 : kTileN) * kTileK * 2;
+    static constexpr int kStageBytes = kBytesA + kBytesB;
+    static constexpr int kStages = 6 * 32768 / kStageBytes;
+    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static constexpr int kTileM = kPair ? 2 * kRows : kRows;
+    static constexpr int kCtas = kPair ? 2 : 1;
+};
 constexpr int kMaxCtas = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kAlign = 256;
@@ -75,8 +93,7 @@ struct GemmArgs {
     int32_t target_bytes;
     int64_t ignore;
     // kLoss
-    float2* part;         // [n][part_ld]: maximum and sum of a tile's row
-    float* zt;            // [n]: the target's logit
+    float2* part;         // [n][part_ld]: maximum and sum of 128 columns
     int32_t part_ld;
     int32_t* status;      // one per CTA: 1 after a wait that ran out
     // kDz
@@ -138,65 +155,45 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t)
 // results: one thread per row of the tile, 32 columns at a time
 // ---------------------------------------------------------------------------
 
-// Maximum and sum of exponentials of 256 columns; the target's column is left
-// out of the sum and its logit kept.
-__device__ __forceinline__ void rows_loss(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+// Maximum and sum of exponentials of 128 columns; the target's column is left
+// out.
+__device__ __forceinline__ void rows_loss(const GemmArgs& g, int col0, int row, float (&z)[kHalf])
 {
-    const int col0 = t.n * kTileN;
     const int64_t target = row < g.n ? target_of(g, row) : -1;
-    const int cols = min(kTileN, g.v - col0);
     const int64_t hit64 = target - col0;
-    const int hit = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < kTileN ? (int)hit64 : -1;
-    float top = -INFINITY, sum = 0.0f, zt = 0.0f;
-    uint32_t r[32];
-#pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
-        if (c >= cols)
-            break;
-        __syncwarp();
-        tmem_load32(tmem + c, r);
-        tmem_wait_load(r);
-        float* z = reinterpret_cast<float*>(r);
-        if (c + 32 > cols) {
+    const bool hits = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < kHalf;
+    const int hit = hits ? (int)hit64 : -1;
+    const int cols = min(kHalf, g.v - col0);
+    if (cols < kHalf) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                z[k] = c + k < cols ? z[k] : -INFINITY;
-        }
-        if (__any_sync(0xffffffffu, hit >= c && hit < c + 32)) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const bool here = c + k == hit;
-                zt = here ? z[k] : zt;
-                z[k] = here ? -INFINITY : z[k];
-            }
-        }
-        float m4[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-        for (int k = 4; k < 32; ++k)
-            m4[k & 3] = fmaxf(m4[k & 3], z[k]);
-        const float now = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), top);
-        // a row of nothing but -inf sums to zero: no inf - inf
-        const float base = now == -INFINITY ? 0.0f : now * kLog2e;
-        float s4[4] = {sum * exp2_fast(fmaf(top, kLog2e, -base)), 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
-        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        top = now;
+        for (int k = 0; k < kHalf; ++k)
+            z[k] = k < cols ? z[k] : -INFINITY;
     }
-    if (row < g.n) {
-        g.part[(int64_t)row * g.part_ld + t.n] = make_float2(top, sum);
-        if (hit >= 0)
-            g.zt[row] = zt;
+    if (__any_sync(0xffffffffu, hit >= 0)) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+            z[k] = k == hit ? -INFINITY : z[k];
     }
+    float m4[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+    for (int k = 4; k < kHalf; ++k)
+        m4[k & 3] = fmaxf(m4[k & 3], z[k]);
+    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    // a row of nothing but -inf sums to zero: no inf - inf
+    const float base = top == -INFINITY ? 0.0f : top * kLog2e;
+    float s4[4] = {};
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k)
+        s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
+    if (row < g.n && cols > 0)
+        g.part[(int64_t)row * g.part_ld + col0 / kHalf] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
-// dz of 256 columns, rounded to 16 bits once.
+// dz of 128 columns, rounded to 16 bits once.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dz(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, uint32_t tmem, int row)
 {
-    const int col0 = t.n * kTileN;               // inside the piece
-    const int cols = min(kTileN, g.v - g.col0 - col0);
+    const int cols = min(kHalf, g.v - g.col0 - col0);  // col0 counts inside the piece
     float base = 0.0f, at_target = 0.0f;
     int hit = -1;
     bool live = false;
@@ -206,12 +203,12 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, const Tile& t, uint32
         base = fmaf(-g.stats.lse[row], kLog2e, g.exponent);
         at_target = ldexpf(expm1f(-g.stats.loss[row]), (int)g.exponent);
         const int64_t h = target - g.col0 - col0;
-        hit = live && target >= 0 && target < g.v && h >= 0 && h < kTileN ? (int)h : -1;
+        hit = live && target >= 0 && target < g.v && h >= 0 && h < kHalf ? (int)h : -1;
     }
     uint16_t* out = g.dz + (int64_t)row * g.dz_ld + col0;
     uint32_t r[32];
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
+    for (int c = 0; c < kHalf; c += 32) {
         __syncwarp();
         tmem_load32(tmem + c, r);
         tmem_wait_load(r);
@@ -243,14 +240,13 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, const Tile& t, uint32
     }
 }
 
-// 256 columns of dH's binary32 sums (d is a multiple of 8).
-__device__ __forceinline__ void rows_dh(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+// 128 columns of dH's binary32 sums (d is a multiple of 8).
+__device__ __forceinline__ void rows_dh(const GemmArgs& g, int split, int col0, uint32_t tmem, int row)
 {
-    const int col0 = t.n * kTileN;
-    float* out = g.dh + ((int64_t)t.split * g.n + row) * g.d + col0;
+    float* out = g.dh + ((int64_t)split * g.n + row) * g.d + col0;
     uint32_t r[32];
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
+    for (int c = 0; c < kHalf; c += 32) {
         if (col0 + c >= g.d)
             break;
         __syncwarp();
@@ -277,16 +273,15 @@ __device__ __forceinline__ void rows_dh(const GemmArgs& g, const Tile& t, uint32
     }
 }
 
-// 256 columns of dW, final.
+// 128 columns of dW, final.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dw(const GemmArgs& g, const Tile& t, uint32_t tmem, int row)
+__device__ __forceinline__ void rows_dw(const GemmArgs& g, int col0, uint32_t tmem, int row)
 {
-    const int col0 = t.n * kTileN;
     const float scale = *g.gscale;
     uint16_t* out = g.dw + (int64_t)row * g.dw_ld + col0;
     uint32_t r[32];
 #pragma unroll 1
-    for (int c = 0; c < kTileN; c += 32) {
+    for (int c = 0; c < kHalf; c += 32) {
         if (col0 + c >= g.d)
             break;
         __syncwarp();
@@ -320,142 +315,204 @@ __device__ __forceinline__ void rows_dw(const GemmArgs& g, const Tile& t, uint32
 // the product kernel
 // ---------------------------------------------------------------------------
 
-template <int kMode, bool kBf16>
+template <bool kPair, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
 {
+    using S = Shape<kPair>;
     extern __shared__ uint8_t dyn[];
-    __shared__ alignas(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_drain;
+    __shared__ alignas(8) uint64_t s_full[S::kStages], s_empty[S::kStages], s_acc_full[2], s_acc_empty[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tiles_at = (smem_addr(dyn) + 1023u) & ~1023u;  // swizzle atoms are 1024 bytes
+    const uint32_t rank = kPair ? cluster_rank() : 0;
+    const int worker = blockIdx.x / S::kCtas, workers = gridDim.x / S::kCtas;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_addr(&s_full[s]), 1);
             mbar_init(smem_addr(&s_empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&s_acc_full[b]), 1);
-            mbar_init(smem_addr(&s_acc_empty[b]), 4);
+            mbar_init(smem_addr(&s_acc_empty[b]), kResultWarps * S::kCtas);
         }
         mbar_init(smem_addr(&s_drain), 1);
         s_dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 2)
-        tmem_alloc(smem_addr(&s_tmem), 512);
+    if (warp == 0)
+        tmem_alloc<kPair>(smem_addr(&s_tmem), 512);
     fence_before_sync();
     __syncthreads();
+    if constexpr (kPair)
+        cluster_sync();
     fence_after_sync();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
+    const int promote = kMode == kLoss ? kPromote : 0x7fffffff;
 
-    if (warp == 0 && lane == 0) {
-        // ---- loads
+    if (warp == kResultWarps && lane == 0) {
+        // ---- loads: this CTA's rows of A and its share of the columns of B
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+        for (int t = worker; ok && t < g.tiles; t += workers) {
             const Tile u = tile_at(g, t);
             const Job& j = g.job[u.job];
             const CUtensorMap* ma = &g.a[u.job];
             const CUtensorMap* mb = &g.b[u.job];
+            const int row0 = u.m * S::kTileM + (int)rank * kRows;
+            const int col0 = u.n * kTileN + (int)rank * kHalf;
             for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-                const uint32_t s = it % kStages, phase = (it / kStages) & 1;
+                const uint32_t s = it % S::kStages, phase = (it / S::kStages) & 1;
                 if (!(ok = mbar_wait(smem_addr(&s_empty[s]), phase ^ 1, dead)))
                     break;
-                const uint32_t full = smem_addr(&s_full[s]);
-                const uint32_t at_a = tiles_at + s * kStageBytes, at_b = at_a + kBytesA;
-                mbar_expect(full, kStageBytes);
+                uint32_t full = smem_addr(&s_full[s]);
+                const uint32_t at_a = tiles_at + s * S::kStageBytes, at_b = at_a + kBytesA;
+                if (rank == 0)
+                    mbar_expect(full, S::kStageBytes * S::kCtas);
+                if constexpr (kPair)
+                    full = peer_addr(full, 0);
+                auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
+                    if constexpr (kPair)
+                        tma_load_pair(at, m, full, x, y);
+                    else
+                        tma_load(at, m, full, x, y);
+                };
                 if (j.a_mn) {
-                    for (int q = 0; q < kTileM / 64; ++q)
-                        tma_load(at_a + q * (64 * kTileK * 2), ma, full, u.m * kTileM + q * 64, kb * kTileK);
+                    for (int q = 0; q < kRows / 64; ++q)
+                        load(at_a + q * (64 * kTileK * 2), ma, row0 + q * 64, kb * kTileK);
                 } else {
-                    tma_load(at_a, ma, full, kb * kTileK, u.m * kTileM);
+                    load(at_a, ma, kb * kTileK, row0);
                 }
                 if (j.b_mn) {
-                    for (int q = 0; q < kTileN / 64; ++q)
-                        tma_load(at_b + q * (64 * kTileK * 2), mb, full, u.n * kTileN + q * 64, kb * kTileK);
+                    for (int q = 0; q < kTileN / S::kCtas / 64; ++q)
+                        load(at_b + q * (64 * kTileK * 2), mb, col0 + q * 64, kb * kTileK);
                 } else {
-                    tma_load(at_b, mb, full, kb * kTileK, u.n * kTileN);
+                    for (int q = 0; q < 2 / S::kCtas; ++q)
+                        load(at_b + q * (kHalf * kTileK * 2), mb, kb * kTileK, col0 + q * kHalf);
                 }
             }
         }
-        if (!ok) {  // let the loads in flight land before the block leaves
-            for (uint32_t b = it > kStages ? it - kStages : 0; b < it; ++b)
-                mbar_wait(smem_addr(&s_full[b % kStages]), (b / kStages) & 1, nullptr);
+        // the last products' signals must find this block's barriers
+        for (uint32_t b = it > S::kStages ? it - S::kStages : 0; ok && b < it; ++b)
+            ok = mbar_wait(smem_addr(&s_empty[b % S::kStages]), (b / S::kStages) & 1, dead);
+        if (!ok && rank == 0) {  // let the loads in flight land before the block leaves
+            for (uint32_t b = it > S::kStages ? it - S::kStages : 0; b < it; ++b)
+                mbar_wait(smem_addr(&s_full[b % S::kStages]), (b / S::kStages) & 1, nullptr);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == kResultWarps + 1 && lane == 0 && rank == 0) {
         // ---- products
         uint32_t it = 0, acc = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < g.tiles; t += gridDim.x, ++acc) {
+        for (int t = worker; ok && t < g.tiles; t += workers) {
             const Tile u = tile_at(g, t);
             const Job& j = g.job[u.job];
-            const uint32_t buf = acc & 1;
-            if (!(ok = mbar_wait(smem_addr(&s_acc_empty[buf]), ((acc >> 1) & 1) ^ 1, dead)))
-                break;
-            fence_after_sync();
-            const uint32_t d = tmem + buf * kTileN;
             // one product takes 16 of K: 32 bytes along a row, or 16 rows
             const uint32_t step_a = j.a_mn ? 2048 : 32, step_b = j.b_mn ? 2048 : 32;
             const uint32_t block = 64 * kTileK * 2;
-            for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-                const uint32_t s = it % kStages;
-                if (!(ok = mbar_wait(smem_addr(&s_full[s]), (it / kStages) & 1, dead)))
+            for (int kb = u.kb0; ok && kb < u.kb1; ++acc) {
+                const uint32_t buf = acc & 1;
+                if (!(ok = mbar_wait(smem_addr(&s_acc_empty[buf]), ((acc >> 1) & 1) ^ 1, dead)))
                     break;
                 fence_after_sync();
-                const uint32_t at_a = tiles_at + s * kStageBytes, at_b = at_a + kBytesA;
+                const uint32_t d = tmem + buf * kTileN;
+                const int first = kb, last = min(u.kb1 - kb, promote) + kb;
+                for (; kb < last; ++kb, ++it) {
+                    const uint32_t s = it % S::kStages;
+                    if (!(ok = mbar_wait(smem_addr(&s_full[s]), (it / S::kStages) & 1, dead)))
+                        break;
+                    fence_after_sync();
+                    const uint32_t at_a = tiles_at + s * S::kStageBytes, at_b = at_a + kBytesA;
 #pragma unroll
-                for (int k = 0; k < kTileK / 16; ++k)
-                    mma_f16(d, smem_desc(at_a + k * step_a, block, 1024), smem_desc(at_b + k * step_b, block, 1024),
-                            j.idesc, kb > u.kb0 || k > 0);
-                mma_commit(smem_addr(&s_empty[s]));
+                    for (int k = 0; k < kTileK / 16; ++k)
+                        mma_f16<kPair>(d, smem_desc(at_a + k * step_a, block, 1024),
+                                       smem_desc(at_b + k * step_b, block, 1024), j.idesc, kb > first || k > 0);
+                    mma_commit<kPair>(smem_addr(&s_empty[s]));
+                }
+                if (ok)
+                    mma_commit<kPair>(smem_addr(&s_acc_full[buf]));
             }
-            if (ok)
-                mma_commit(smem_addr(&s_acc_full[buf]));
         }
         if (!ok) {  // let the products in flight end before tensor memory is freed
-            mma_commit(smem_addr(&s_drain));
+            mma_commit<kPair>(smem_addr(&s_drain));
             mbar_wait(smem_addr(&s_drain), 0, nullptr);
         }
-    } else if (warp >= 4) {
+    } else if (warp < kResultWarps) {
         // ---- results
         const int quad = warp & 3;  // a warp reads the 32 lanes of its quarter
+        const int half = warp >> 2;
+        const uint32_t lanes_at = tmem + ((uint32_t)(quad * 32) << 16) + half * kHalf;
         uint32_t acc = 0;
-        for (int t = blockIdx.x; t < g.tiles; t += gridDim.x, ++acc) {
-            const Tile u = tile_at(g, t);
-            const uint32_t buf = acc & 1;
-            const int row = u.m * kTileM + quad * 32 + lane;
-            const bool ok = mbar_wait(smem_addr(&s_acc_full[buf]), (acc >> 1) & 1, dead);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
+        bool ok = true;
+        auto await = [&]() {
+            const bool mine = mbar_wait(smem_addr(&s_acc_full[acc & 1]), (acc >> 1) & 1, dead);
+            ok = __all_sync(0xffffffffu, mine);
             fence_after_sync();
-            const uint32_t at = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-            if constexpr (kMode == kLoss) {
-                rows_loss(g, u, at, row);
-            } else if constexpr (kMode == kDz) {
-                rows_dz<kBf16>(g, u, at, row);
-            } else {
-                if (u.job == 0)
-                    rows_dh(g, u, at, row);
-                else
-                    rows_dw<kBf16>(g, u, at, row);
-            }
+            return ok;
+        };
+        auto give_back = [&]() {
             fence_before_sync();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&s_acc_empty[buf]));
+            if (lane == 0) {
+                const uint32_t bar = smem_addr(&s_acc_empty[acc & 1]);
+                if constexpr (kPair)
+                    mbar_arrive_peer(peer_addr(bar, 0));
+                else
+                    mbar_arrive(bar);
+            }
+            ++acc;
+        };
+        for (int t = worker; ok && t < g.tiles; t += workers) {
+            const Tile u = tile_at(g, t);
+            const int row = u.m * S::kTileM + (int)rank * kRows + quad * 32 + lane;
+            const int col0 = u.n * kTileN + half * kHalf;
+            if constexpr (kMode == kLoss) {
+                float z[kHalf];
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k)
+                    z[k] = 0.0f;
+                for (int kb = u.kb0; ok && kb < u.kb1; kb += kPromote) {
+                    if (!await())
+                        break;
+                    const uint32_t at = lanes_at + (acc & 1) * kTileN;
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 16) {
+                        uint32_t r[16];
+                        tmem_load16(at + c, r);
+                        tmem_wait_load(r);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            z[c + k] += __uint_as_float(r[k]);
+                    }
+                    give_back();
+                }
+                if (ok)
+                    rows_loss(g, col0, row, z);
+            } else {
+                if (!await())
+                    break;
+                const uint32_t at = lanes_at + (acc & 1) * kTileN;
+                if constexpr (kMode == kDz)
+                    rows_dz<kBf16>(g, col0, at, row);
+                else if (u.job == 0)
+                    rows_dh(g, u.split, col0, at, row);
+                else
+                    rows_dw<kBf16>(g, col0, at, row);
+                give_back();
+            }
         }
     }
     __syncwarp();
     fence_before_sync();
     __syncthreads();
+    if constexpr (kPair)
+        cluster_sync();  // no CTA leaves while its pair may still signal it
     fence_after_sync();
-    if (warp == 2)
-        tmem_free(tmem, 512);
+    if (warp == 0)
+        tmem_free<kPair>(tmem, 512);
     if (threadIdx.x == 0) {
         if constexpr (kMode == kLoss)
             g.status[blockIdx.x] = s_dead;
@@ -475,8 +532,48 @@ struct MergePart {
 
 constexpr int kMergeRows = 8;  // rows (warps) per CTA
 
+// The logit of one row's target, d values in binary32 with rounding to
+// nearest: a loss is mostly the distance from it.
+template <bool kBf16>
+__device__ __forceinline__ float target_logit(const uint16_t* h, const uint16_t* w, int d, int lane)
+{
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int k = lane * 8; k < d; k += 256) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(h + k)), b = __ldg(reinterpret_cast<const uint4*>(w + k));
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float2 p, q;
+            if constexpr (kBf16) {
+                p = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u));
+                q = make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u));
+            } else {
+                p = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+                q = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+            }
+            s0 = fmaf(p.x, q.x, s0);
+            s1 = fmaf(p.y, q.y, s1);
+        }
+    }
+    float s = s0 + s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+struct MergeArgs {
+    const uint16_t* hidden;
+    const uint16_t* weight;
+    int64_t ld_hidden, ld_weight;
+    float* token_loss;
+    float* lse;
+    MergePart* out;
+};
+
+template <bool kBf16>
 __global__ void __launch_bounds__(kMergeRows * 32)
-xent_merge_kernel(GemmArgs g, float* token_loss, float* lse, MergePart* out)
+xent_merge_kernel(const __grid_constant__ GemmArgs g, MergeArgs a)
 {
     __shared__ float s_loss[kMergeRows];
     __shared__ int s_valid[kMergeRows];
@@ -505,7 +602,8 @@ xent_merge_kernel(GemmArgs g, float* token_loss, float* lse, MergePart* out)
         valid = t != g.ignore;
         if (valid) {
             if (t >= 0 && t < g.v) {
-                const float zt = g.zt[row];
+                const float zt = target_logit<kBf16>(a.hidden + (int64_t)row * a.ld_hidden, a.weight + t * a.ld_weight,
+                                                     g.d, lane);
                 const float over = others - zt;
                 loss = fmaxf(over, 0.0f) + log1pf(expf(-fabsf(over)));
                 if (isnan(over))
@@ -516,8 +614,8 @@ xent_merge_kernel(GemmArgs g, float* token_loss, float* lse, MergePart* out)
             }
         }
         if (lane == 0) {
-            token_loss[row] = loss;
-            lse[row] = total;
+            a.token_loss[row] = loss;
+            a.lse[row] = total;
         }
     }
     if (lane == 0) {
@@ -531,7 +629,7 @@ xent_merge_kernel(GemmArgs g, float* token_loss, float* lse, MergePart* out)
             m.loss += (double)s_loss[k];
             m.valid += (unsigned long long)s_valid[k];
         }
-        out[blockIdx.x] = m;
+        a.out[blockIdx.x] = m;
     }
 }
 
@@ -643,11 +741,11 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 struct Plan {
     bool grad = false, want_dh = false, want_dw = false;
-    int64_t vtiles = 0;     // 256-column tiles of the whole vocabulary
+    int64_t parts = 0;      // 128-column parts of the whole vocabulary
     int64_t piece = 0;      // columns of one piece of the backward pass
     int64_t splits = 1;     // of dH's sums over a piece
     int64_t merges = 0;
-    size_t off_part = 0, off_zt = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
+    size_t off_part = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
            off_dh = 0, total = 0;
 };
 
@@ -659,7 +757,7 @@ int make_plan(const mpt_xent_args& a, Plan& p)
     p.want_dh = a.grad_hidden != nullptr;
     p.want_dw = a.grad_weight != nullptr;
     p.grad = p.want_dh || p.want_dw;
-    p.vtiles = ceil_div(a.v, kTileN);
+    p.parts = ceil_div(a.v, kHalf);
     p.merges = ceil_div(a.n, kMergeRows);
     size_t at = 0;
     auto region = [&](size_t bytes) {
@@ -668,8 +766,7 @@ int make_plan(const mpt_xent_args& a, Plan& p)
         return here;
     };
     p.off_ctl = region(256 + sizeof(int32_t) * kMaxCtas);
-    p.off_part = region(sizeof(float2) * (size_t)(a.n * p.vtiles));
-    p.off_zt = region(sizeof(float) * (size_t)a.n);
+    p.off_part = region(sizeof(float2) * (size_t)(a.n * p.parts));
     p.off_token = region(sizeof(float) * (size_t)a.n);
     p.off_lse = region(sizeof(float) * (size_t)a.n);
     p.off_merge = region(sizeof(MergePart) * (size_t)p.merges);
@@ -680,8 +777,8 @@ int make_plan(const mpt_xent_args& a, Plan& p)
         if (p.want_dh) {
             // cut dH's sums so that one tile is at most half a CTA's share of the piece's work
             const int64_t kb_v = ceil_div(p.piece, kTileK), kb_n = ceil_div(a.n, kTileK);
-            const int64_t tiles_h = ceil_div(a.n, kTileM) * ceil_div(a.d, kTileN);
-            const int64_t tiles_w = p.want_dw ? ceil_div(p.piece, kTileM) * ceil_div(a.d, kTileN) : 0;
+            const int64_t tiles_h = ceil_div(a.n, kRows) * ceil_div(a.d, kTileN);
+            const int64_t tiles_w = p.want_dw ? ceil_div(p.piece, kRows) * ceil_div(a.d, kTileN) : 0;
             const int64_t share = (tiles_h * kb_v + tiles_w * kb_n) / kMaxCtas;
             p.splits = std::min<int64_t>(64, ceil_div(kb_v, std::max<int64_t>(8, share / 2)));
             p.off_dh = region((size_t)(p.splits * a.n * a.d * 4));
@@ -702,8 +799,8 @@ bool args_ok(const mpt_xent_args* a)
     if (a->reduction != MPT_XENT_MEAN && a->reduction != MPT_XENT_SUM)
         return false;
     // tiles are counted in 31 bits
-    const int64_t most = (int64_t)1 << 30, rows = ceil_div(a->n, kTileM), wide = ceil_div(a->d, kTileN);
-    return rows * ceil_div(a->v, kTileN) <= most && rows * wide * 64 <= most && ceil_div(a->v, kTileM) * wide <= most;
+    const int64_t most = (int64_t)1 << 30, rows = ceil_div(a->n, kRows), wide = ceil_div(a->d, kTileN);
+    return rows * ceil_div(a->v, kTileN) <= most && rows * wide * 64 <= most && ceil_div(a->v, kRows) * wide <= most;
 }
 
 // [lo, hi) of rows of d 16-bit values ld apart
@@ -774,29 +871,45 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t co
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kMode, bool kBf16>
-cudaError_t launch_product(const GemmArgs& g, cudaStream_t st)
+template <bool kPair, int kMode, bool kBf16>
+cudaError_t launch_shape(const GemmArgs& g, cudaStream_t st)
 {
-    cudaError_t e = cudaFuncSetAttribute(xent_product_kernel<kMode, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    using S = Shape<kPair>;
+    const cudaError_t e = cudaFuncSetAttribute(xent_product_kernel<kPair, kMode, kBf16>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)std::min(g.tiles, kMaxCtas));
+    lc.gridDim = dim3((unsigned)std::min(g.tiles * S::kCtas, kMaxCtas));
     lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = kSmem;
+    lc.dynamicSmemBytes = S::kSmem;
     lc.stream = st;
-    return cudaLaunchKernelEx(&lc, xent_product_kernel<kMode, kBf16>, g);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S::kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, xent_product_kernel<kPair, kMode, kBf16>, g);
 }
 
-void set_job(Job& j, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn)
+template <int kMode, bool kBf16>
+cudaError_t launch_product(bool pair, const GemmArgs& g, cudaStream_t st)
 {
-    j.mt = (int32_t)ceil_div(m, kTileM);
+    return pair ? launch_shape<true, kMode, kBf16>(g, st) : launch_shape<false, kMode, kBf16>(g, st);
+}
+
+void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn)
+{
+    const int rows = pair ? 2 * kRows : kRows;
+    j.mt = (int32_t)ceil_div(m, rows);
     j.nt = (int32_t)ceil_div(n, kTileN);
     j.kb = (int32_t)ceil_div(k, kTileK);
     j.splits = (int32_t)std::min<int64_t>(splits, j.kb);
     j.a_mn = a_mn;
     j.b_mn = b_mn;
-    j.idesc = mma_desc(bf16, a_mn, b_mn, kTileM, kTileN);
+    j.idesc = mma_desc(bf16, a_mn, b_mn, rows, kTileN);
     j.tiles = j.mt * j.nt * j.splits;
 }
 
@@ -808,6 +921,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     float* token = a.token_loss ? a.token_loss : reinterpret_cast<float*>(ws + p.off_token);
     float* lse = a.lse ? a.lse : reinterpret_cast<float*>(ws + p.off_lse);
     const int exponent = kBf16 ? 0 : 15;
+    const bool pair = a.n > kRows;
 
     GemmArgs g{};
     g.n = (int32_t)a.n;
@@ -817,8 +931,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     g.target_bytes = a.target_bytes;
     g.ignore = a.ignore_index;
     g.part = reinterpret_cast<float2*>(ws + p.off_part);
-    g.zt = reinterpret_cast<float*>(ws + p.off_zt);
-    g.part_ld = (int32_t)p.vtiles;
+    g.part_ld = (int32_t)p.parts;
     g.status = status;
     g.stats = {lse, token};
     g.exponent = (float)exponent;
@@ -837,15 +950,17 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     f.parts = reinterpret_cast<MergePart*>(ws + p.off_merge);
 
     if (a.n > 0) {
-        set_job(g.job[0], kBf16, a.n, a.v, a.d, 1, false, false);
+        set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false);
         g.tiles = g.job[0].tiles;
-        if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileM) ||
-            !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, kTileN))
+        if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows) ||
+            !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, kHalf))
             return MPT_ERR_CUDA;
-        if (launch_product<kLoss, kBf16>(g, st) != cudaSuccess)
+        if (launch_product<kLoss, kBf16>(pair, g, st) != cudaSuccess)
             return MPT_ERR_CUDA;
-        f.nstatus = std::min(g.tiles, kMaxCtas);
-        xent_merge_kernel<<<(unsigned)p.merges, kMergeRows * 32, 0, st>>>(g, token, lse, const_cast<MergePart*>(f.parts));
+        f.nstatus = std::min(g.tiles * (pair ? 2 : 1), kMaxCtas);
+        const MergeArgs m{static_cast<const uint16_t*>(a.hidden), static_cast<const uint16_t*>(a.weight), a.ld_hidden,
+                          a.ld_weight, token, lse, const_cast<MergePart*>(f.parts)};
+        xent_merge_kernel<kBf16><<<(unsigned)p.merges, kMergeRows * 32, 0, st>>>(g, m);
         f.nparts = (int32_t)p.merges;
     }
     xent_final_kernel<<<1, 256, 0, st>>>(f);
@@ -875,26 +990,26 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
         const int64_t cols = std::min(p.piece, a.v - c0);
         const uint16_t* wp = w + c0 * a.ld_weight;
         z.col0 = (int32_t)c0;
-        set_job(z.job[0], kBf16, a.n, cols, a.d, 1, false, false);
+        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false);
         z.tiles = z.job[0].tiles;
-        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kTileN))
+        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kHalf))
             return MPT_ERR_CUDA;
-        if (launch_product<kDz, kBf16>(z, st) != cudaSuccess)
+        if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
             return MPT_ERR_CUDA;
 
         // columns beyond `cols` up to the tile's end are zeros in dz
         q.job[0] = q.job[1] = Job{};
         if (p.want_dh) {
-            set_job(q.job[0], kBf16, a.n, a.d, cols, p.splits, false, true);
+            set_job(q.job[0], pair, kBf16, a.n, a.d, cols, p.splits, false, true);
             // (a short last piece may add to the first sums only)
             splits = std::max(splits, q.job[0].splits);
-            if (!make_map(&q.a[0], kBf16, dz, a.n, cols, p.piece, kTileM) ||
+            if (!make_map(&q.a[0], kBf16, dz, a.n, cols, p.piece, kRows) ||
                 !make_map(&q.b[0], kBf16, wp, cols, a.d, a.ld_weight, kTileK))
                 return MPT_ERR_CUDA;
             q.add = c0 > 0;
         }
         if (p.want_dw) {
-            set_job(q.job[1], kBf16, cols, a.d, a.n, 1, true, true);
+            set_job(q.job[1], pair, kBf16, cols, a.d, a.n, 1, true, true);
             if (!make_map(&q.a[1], kBf16, dz, a.n, cols, p.piece, kTileK) ||
                 !make_map(&q.b[1], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK))
                 return MPT_ERR_CUDA;
@@ -902,7 +1017,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
             q.dw_rows = (int32_t)cols;
         }
         q.tiles = q.job[0].tiles + q.job[1].tiles;
-        if (launch_product<kGrad, kBf16>(q, st) != cudaSuccess)
+        if (launch_product<kGrad, kBf16>(pair, q, st) != cudaSuccess)
             return MPT_ERR_CUDA;
     }
     if (p.want_dh) {
