@@ -73,7 +73,6 @@ enum Mode { kLoss, kDz, kGrad };
 // sum cut into `splits` parts.
 struct Job {
     int32_t mt, nt, splits, kb;
-    int32_t a_mn, b_mn;   // operand major-ness
     uint32_t idesc;
     int32_t tiles;
 };
@@ -315,6 +314,37 @@ __device__ __forceinline__ void rows_dw(const GemmArgs& g, int col0, uint32_t tm
 // the product kernel
 // ---------------------------------------------------------------------------
 
+constexpr uint32_t kBlock = 64 * kTileK * 2;  // of 64 M or N elements of an MN-major tile
+
+// Place in a ring of load stages.
+template <int kStages> struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == kStages) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <bool kValue> struct Flag {
+    static constexpr bool value = kValue;
+};
+
+// f(A is MN-major, B is MN-major) of the job: logits are rows times rows, dH
+// is dz's rows times W's columns, dW dz's columns times H's columns.
+template <int kMode, class F>
+__device__ __forceinline__ void by_layout(int job, F&& f)
+{
+    if constexpr (kMode != kGrad)
+        f(Flag<false>{}, Flag<false>{});
+    else if (job == 0)
+        f(Flag<false>{}, Flag<true>{});
+    else
+        f(Flag<true>{}, Flag<true>{});
+}
+
 template <bool kPair, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
 {
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const uint32_t tiles_at = (smem_addr(dyn) + 1023u) & ~1023u;  // swizzle atoms are 1024 bytes
     const uint32_t rank = kPair ? cluster_rank() : 0;
     const int worker = blockIdx.x / S::kCtas, workers = gridDim.x / S::kCtas;
@@ -352,92 +382,124 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     fence_after_sync();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
-    const int promote = kMode == kLoss ? kPromote : 0x7fffffff;
 
-    if (warp == kResultWarps && lane == 0) {
+    // The loading and the multiplying warp run their loops as whole warps, so
+    // that addresses and descriptors stay in uniform registers, and one lane
+    // issues; a step has 512 clocks, and every instruction on the way to its
+    // four products counts (650 clocks a step with one lane in the loop).
+    if (warp == kResultWarps) {
         // ---- loads: this CTA's rows of A and its share of the columns of B
-        uint32_t it = 0;
+        Ring<S::kStages> ring;
+        uint32_t steps = 0;
         bool ok = true;
+        const bool one = elect_one();
         for (int t = worker; ok && t < g.tiles; t += workers) {
             const Tile u = tile_at(g, t);
-            const Job& j = g.job[u.job];
             const CUtensorMap* ma = &g.a[u.job];
             const CUtensorMap* mb = &g.b[u.job];
             const int row0 = u.m * S::kTileM + (int)rank * kRows;
             const int col0 = u.n * kTileN + (int)rank * kHalf;
-            for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-                const uint32_t s = it % S::kStages, phase = (it / S::kStages) & 1;
-                if (!(ok = mbar_wait(smem_addr(&s_empty[s]), phase ^ 1, dead)))
-                    break;
-                uint32_t full = smem_addr(&s_full[s]);
-                const uint32_t at_a = tiles_at + s * S::kStageBytes, at_b = at_a + kBytesA;
-                if (rank == 0)
-                    mbar_expect(full, S::kStageBytes * S::kCtas);
-                if constexpr (kPair)
-                    full = peer_addr(full, 0);
-                auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
-                    if constexpr (kPair)
-                        tma_load_pair(at, m, full, x, y);
-                    else
-                        tma_load(at, m, full, x, y);
-                };
-                if (j.a_mn) {
-                    for (int q = 0; q < kRows / 64; ++q)
-                        load(at_a + q * (64 * kTileK * 2), ma, row0 + q * 64, kb * kTileK);
-                } else {
-                    load(at_a, ma, kb * kTileK, row0);
+            auto run = [&](auto a_mn, auto b_mn) {
+                for (int kb = u.kb0; kb < u.kb1; ++kb, ++steps, ring.next()) {
+                    if (!(ok = mbar_wait(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead)))
+                        break;
+                    if (one) {
+                        uint32_t full = smem_addr(s_full) + ring.at * 8;
+                        const uint32_t at_a = tiles_at + ring.at * S::kStageBytes, at_b = at_a + kBytesA;
+                        if (rank == 0)
+                            mbar_expect(full, S::kStageBytes * S::kCtas);
+                        if constexpr (kPair)
+                            full = peer_addr(full, 0);
+                        auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
+                            if constexpr (kPair)
+                                tma_load_pair(at, m, full, x, y);
+                            else
+                                tma_load(at, m, full, x, y);
+                        };
+                        if constexpr (a_mn.value) {
+#pragma unroll
+                            for (int q = 0; q < kRows / 64; ++q)
+                                load(at_a + q * kBlock, ma, row0 + q * 64, kb * kTileK);
+                        } else {
+                            load(at_a, ma, kb * kTileK, row0);
+                        }
+                        if constexpr (b_mn.value) {
+#pragma unroll
+                            for (int q = 0; q < kTileN / S::kCtas / 64; ++q)
+                                load(at_b + q * kBlock, mb, col0 + q * 64, kb * kTileK);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 2 / S::kCtas; ++q)
+                                load(at_b + q * (kHalf * kTileK * 2), mb, kb * kTileK, col0 + q * kHalf);
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (j.b_mn) {
-                    for (int q = 0; q < kTileN / S::kCtas / 64; ++q)
-                        load(at_b + q * (64 * kTileK * 2), mb, col0 + q * 64, kb * kTileK);
-                } else {
-                    for (int q = 0; q < 2 / S::kCtas; ++q)
-                        load(at_b + q * (kHalf * kTileK * 2), mb, kb * kTileK, col0 + q * kHalf);
-                }
-            }
+            };
+            by_layout<kMode>(u.job, run);
         }
         // the last products' signals must find this block's barriers
-        for (uint32_t b = it > S::kStages ? it - S::kStages : 0; ok && b < it; ++b)
-            ok = mbar_wait(smem_addr(&s_empty[b % S::kStages]), (b / S::kStages) & 1, dead);
+        for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; ok && b < steps; ++b)
+            ok = mbar_wait(smem_addr(s_empty) + (b % S::kStages) * 8, (b / S::kStages) & 1, dead);
         if (!ok && rank == 0) {  // let the loads in flight land before the block leaves
-            for (uint32_t b = it > S::kStages ? it - S::kStages : 0; b < it; ++b)
-                mbar_wait(smem_addr(&s_full[b % S::kStages]), (b / S::kStages) & 1, nullptr);
+            for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; b < steps; ++b)
+                mbar_wait(smem_addr(s_full) + (b % S::kStages) * 8, (b / S::kStages) & 1, nullptr);
         }
-    } else if (warp == kResultWarps + 1 && lane == 0 && rank == 0) {
+    } else if (warp == kResultWarps + 1 && rank == 0) {
         // ---- products
-        uint32_t it = 0, acc = 0;
+        Ring<S::kStages> ring;
+        uint32_t acc = 0;
         bool ok = true;
+        const bool one = elect_one();
         for (int t = worker; ok && t < g.tiles; t += workers) {
             const Tile u = tile_at(g, t);
-            const Job& j = g.job[u.job];
-            // one product takes 16 of K: 32 bytes along a row, or 16 rows
-            const uint32_t step_a = j.a_mn ? 2048 : 32, step_b = j.b_mn ? 2048 : 32;
-            const uint32_t block = 64 * kTileK * 2;
-            for (int kb = u.kb0; ok && kb < u.kb1; ++acc) {
-                const uint32_t buf = acc & 1;
-                if (!(ok = mbar_wait(smem_addr(&s_acc_empty[buf]), ((acc >> 1) & 1) ^ 1, dead)))
-                    break;
-                fence_after_sync();
-                const uint32_t d = tmem + buf * kTileN;
-                const int first = kb, last = min(u.kb1 - kb, promote) + kb;
-                for (; kb < last; ++kb, ++it) {
-                    const uint32_t s = it % S::kStages;
-                    if (!(ok = mbar_wait(smem_addr(&s_full[s]), (it / S::kStages) & 1, dead)))
+            const uint32_t idesc = g.job[u.job].idesc;
+            auto run = [&](auto a_mn, auto b_mn) {
+                // one product takes 16 of K: 32 bytes along a row, or 16 rows
+                constexpr uint32_t step_a = (a_mn.value ? 2048 : 32) >> 4, step_b = (b_mn.value ? 2048 : 32) >> 4;
+                const uint64_t desc_a = smem_desc(tiles_at, kBlock, 1024);
+                const uint64_t desc_b = smem_desc(tiles_at + kBytesA, kBlock, 1024);
+                for (int kb = u.kb0; ok && kb < u.kb1; ++acc) {
+                    const uint32_t buf = acc & 1;
+                    if (!(ok = mbar_wait(smem_addr(s_acc_empty) + buf * 8, ((acc >> 1) & 1) ^ 1, dead)))
                         break;
                     fence_after_sync();
-                    const uint32_t at_a = tiles_at + s * S::kStageBytes, at_b = at_a + kBytesA;
+                    const uint32_t d = tmem + buf * kTileN;
+                    const int last = kMode == kLoss ? min(u.kb1 - kb, kPromote) + kb : u.kb1;
+                    uint32_t add = 0;
+                    // whether the next step's tiles are there is asked before
+                    // this step's products are issued
+                    bool there = mbar_try(smem_addr(s_full) + ring.at * 8, ring.phase);
+                    for (; kb < last; ++kb) {
+                        if (!there && !(ok = mbar_wait(smem_addr(s_full) + ring.at * 8, ring.phase, dead)))
+                            break;
+                        fence_after_sync();
+                        const uint32_t here = ring.at;
+                        ring.next();
+                        if (kb + 1 < last)
+                            there = mbar_try(smem_addr(s_full) + ring.at * 8, ring.phase);
+                        const uint64_t a = desc_a + here * (S::kStageBytes >> 4), b = desc_b + here * (S::kStageBytes >> 4);
+                        if (one) {
 #pragma unroll
-                    for (int k = 0; k < kTileK / 16; ++k)
-                        mma_f16<kPair>(d, smem_desc(at_a + k * step_a, block, 1024),
-                                       smem_desc(at_b + k * step_b, block, 1024), j.idesc, kb > first || k > 0);
-                    mma_commit<kPair>(smem_addr(&s_empty[s]));
+                            for (int k = 0; k < kTileK / 16; ++k) {
+                                mma_f16<kPair>(d, a + k * step_a, b + k * step_b, idesc, add);
+                                add = 1;
+                            }
+                            mma_commit<kPair>(smem_addr(s_empty) + here * 8);
+                        }
+                        add = 1;
+                        __syncwarp();
+                    }
+                    if (ok && one)
+                        mma_commit<kPair>(smem_addr(s_acc_full) + buf * 8);
+                    __syncwarp();
                 }
-                if (ok)
-                    mma_commit<kPair>(smem_addr(&s_acc_full[buf]));
-            }
+            };
+            by_layout<kMode>(u.job, run);
         }
         if (!ok) {  // let the products in flight end before tensor memory is freed
-            mma_commit<kPair>(smem_addr(&s_drain));
+            if (one)
+                mma_commit<kPair>(smem_addr(&s_drain));
             mbar_wait(smem_addr(&s_drain), 0, nullptr);
         }
     } else if (warp < kResultWarps) {
@@ -907,8 +969,6 @@ void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int6
     j.nt = (int32_t)ceil_div(n, kTileN);
     j.kb = (int32_t)ceil_div(k, kTileK);
     j.splits = (int32_t)std::min<int64_t>(splits, j.kb);
-    j.a_mn = a_mn;
-    j.b_mn = b_mn;
     j.idesc = mma_desc(bf16, a_mn, b_mn, rows, kTileN);
     j.tiles = j.mt * j.nt * j.splits;
 }

@@ -16,6 +16,14 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// The warp's number as a value that the compiler knows to be the same in all
+// of its lanes.
+__device__ __forceinline__ int warp_number()
+{
+    return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+
+// True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t pred;
@@ -52,27 +60,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-__device__ __forceinline__ uint64_t nanoseconds()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-constexpr uint64_t kWaitLimit = 4000000000ull;  // 4 s: no wait here takes a millisecond
+// Waits are bounded by the clock.
+constexpr long long kWaitLimit = 8000000000ll;  // clocks, some 4 s: no wait here takes a millisecond
 
 // Wait for the phase of the given parity; false once the block is dead, or
 // (dead == nullptr: the drain before the block leaves) after the limit.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead)
 {
-    uint64_t began = 0;
+    long long began = 0;
     for (uint32_t i = 0;; ++i) {
         if (mbar_try(bar, parity))
             return true;
         if ((i & 63u) == 63u) {
             if (dead && *dead)
                 return false;
-            const uint64_t now = nanoseconds();
+            const long long now = clock64();
             if (began == 0)
                 began = now;
             if (now - began > kWaitLimit)
@@ -222,17 +224,17 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
 
 // kPair: both CTAs' tiles, issued by the first.
 template <bool kPair>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     if constexpr (kPair)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+                     "l"(a), "l"(b), "r"(idesc), "r"(add)
                      : "memory");
     else
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+                     "l"(a), "l"(b), "r"(idesc), "r"(add)
                      : "memory");
 }
 
