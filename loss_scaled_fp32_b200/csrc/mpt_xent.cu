@@ -54,12 +54,18 @@ constexpr int kHalf = kTileN / 2;       // columns of one result warp
 // 16 bits, need not.
 constexpr int kPromote = 512 / kTileK;
 
+// Results leave through shared memory: each half of the result warps has one
+// box of 128 rows of 128 bytes, which TMA stores.  (Rows stored straight from
+// registers, 16 bytes of 32 rows at a time, cost a tenth of the whole
+// backward pass.)
+constexpr int kOutBytes = kRows * 128;
+
 // Shared memory of one load stage, and how many fit.
 template <bool kPair> struct Shape {
     static constexpr int kBytesB = (kPair ? kTileN / 2 : kTileN) * kTileK * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
     static constexpr int kStages = 6 * 32768 / kStageBytes;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024;
     static constexpr int kTileM = kPair ? 2 * kRows : kRows;
     static constexpr int kCtas = kPair ? 2 : 1;
 };
@@ -70,11 +76,15 @@ constexpr size_t kAlign = 256;
 enum Mode { kLoss, kDz, kGrad };
 
 // One product: mt x nt output tiles, each summed over kb blocks of 64, the
-// sum cut into `splits` parts.
+// sum cut into `splits` parts.  Tiles are taken in bands of `band` rows of
+// tiles, the rows of a band first: what runs at the same time then shares
+// the band's rows of A, held in L2, and few columns of B.  band 1: along a row.
 struct Job {
     int32_t mt, nt, splits, kb;
+    int32_t band;
     uint32_t idesc;
     int32_t tiles;
+    int32_t is_dw;        // kGrad: dW (else dH)
 };
 
 struct RowStats {
@@ -83,9 +93,12 @@ struct RowStats {
 };
 
 struct GemmArgs {
-    CUtensorMap a[2], b[2];
-    Job job[2];           // kGrad: dH, then dW
-    int32_t tiles;
+    CUtensorMap a[2], b[2], out[2];
+    Job job[2];           // kGrad: dH and dW, the longer tiles first
+    // Tile order, worked out by every worker alone: the first job's tiles go
+    // round; `late` workers have one more of them, while they are at it the
+    // others take `ahead` rounds of the second job; then all go round.
+    int32_t late, ahead;
     // rows and columns of the logits
     int32_t n, v;
     const void* targets;
@@ -97,18 +110,15 @@ struct GemmArgs {
     int32_t* status;      // one per CTA: 1 after a wait that ran out
     // kDz
     RowStats stats;
-    uint16_t* dz;         // [n][dz_ld], columns col0 ...
-    int64_t dz_ld;
-    int32_t col0;
+    int32_t col0;         // first column of the piece
     float exponent;       // dz is scaled by 2^exponent
     // kGrad
-    float* dh;            // [splits][n][d] binary32 sums over the pieces
     int32_t d;
-    int32_t add;          // add to what an earlier piece left there
-    uint16_t* dw;         // rows of this piece
+    int32_t add;          // dH: add to what an earlier piece left there
+    uint16_t* dw;         // rows of this piece, where TMA cannot store them
     int64_t dw_ld;
     int32_t dw_rows;
-    int32_t dw_wide;      // 16-byte stores are aligned
+    int32_t dw_wide;      // TMA can
     const float* gscale;
     float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
 };
@@ -135,16 +145,34 @@ struct Tile {
     int job, m, n, split, kb0, kb1;
 };
 
+// The k-th tile of a worker, or -1.
+__device__ __forceinline__ int tile_number(const GemmArgs& g, int worker, int workers, int k)
+{
+    const int first = g.job[0].tiles, second = g.job[1].tiles;
+    if (worker + k * workers < first)
+        return worker + k * workers;
+    if (second == 0)
+        return -1;
+    const bool late = worker < g.late;
+    const int j = k - (first / workers + (late ? 1 : 0));
+    const int early = workers - g.late, base = g.ahead * early;
+    const int i = late ? base + j * workers + worker
+                       : j < g.ahead ? j * early + worker - g.late : base + (j - g.ahead) * workers + worker;
+    return i < second ? first + i : -1;
+}
+
 __device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t)
 {
     Tile r;
     r.job = t >= g.job[0].tiles ? 1 : 0;
     const Job& j = g.job[r.job];
     int i = t - (r.job ? g.job[0].tiles : 0);
-    r.m = i % j.mt;
-    i /= j.mt;
-    r.n = i % j.nt;
-    r.split = i / j.nt;
+    r.split = i / (j.mt * j.nt);
+    i -= r.split * (j.mt * j.nt);
+    const int m0 = i / (j.band * j.nt) * j.band, rows = min(j.band, j.mt - m0);
+    i -= m0 * j.nt;
+    r.n = i / rows;
+    r.m = m0 + i - r.n * rows;
     r.kb0 = (int)((int64_t)j.kb * r.split / j.splits);
     r.kb1 = (int)((int64_t)j.kb * (r.split + 1) / j.splits);
     return r;
@@ -188,11 +216,39 @@ __device__ __forceinline__ void rows_loss(const GemmArgs& g, int col0, int row, 
         g.part[(int64_t)row * g.part_ld + col0 / kHalf] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
+// A result warp's place in its half's box: rows of 128 bytes, the 16-byte
+// pieces of a row exchanged as TMA's 128-byte swizzle does.
+struct Box {
+    uint32_t row_at;      // this thread's row
+    uint32_t at;
+    int row, half;
+    bool first;           // of the half's threads: it stores
+
+    __device__ __forceinline__ void put(int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const
+    {
+        shared_store16(row_at + ((piece ^ (row & 7)) << 4), a, b, c, d);
+    }
+    // before the first put: the last store has read the box
+    __device__ __forceinline__ void open() const
+    {
+        if (first)
+            store_wait_read();
+        named_sync(1 + half, 32 * kResultWarps / 2);
+    }
+    // after the last put; the first thread then stores and commits
+    __device__ __forceinline__ void close() const
+    {
+        fence_async();
+        named_sync(1 + half, 32 * kResultWarps / 2);
+    }
+};
+
 // dz of 128 columns, rounded to 16 bits once.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, uint32_t tmem, int row)
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int row0, uint32_t tmem, const Box& box)
 {
     const int cols = min(kHalf, g.v - g.col0 - col0);  // col0 counts inside the piece
+    const int row = row0 + box.row;
     float base = 0.0f, at_target = 0.0f;
     int hit = -1;
     bool live = false;
@@ -204,107 +260,113 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, uint32_t tm
         const int64_t h = target - g.col0 - col0;
         hit = live && target >= 0 && target < g.v && h >= 0 && h < kHalf ? (int)h : -1;
     }
-    uint16_t* out = g.dz + (int64_t)row * g.dz_ld + col0;
-    uint32_t r[32];
+    const bool any_dead = !__all_sync(0xffffffffu, live);
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
-        __syncwarp();
-        tmem_load32(tmem + c, r);
-        tmem_wait_load(r);
-        float* z = reinterpret_cast<float*>(r);
+    for (int c = 0; c < kHalf; c += 64) {
+        box.open();
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-            z[k] = exp2_fast(fmaf(z[k], kLog2e, base));
-        if (c + 32 > cols || !live) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                z[k] = live && c + k < cols ? z[k] : 0.0f;
-        }
-        if (hit >= c && hit < c + 32) {
+        for (int q = 0; q < 64; q += 32) {
+            uint32_t r[32];
+            tmem_load32(tmem + c + q, r);
+            tmem_wait_load(r);
+            float* z = reinterpret_cast<float*>(r);
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-                z[k] = c + k == hit ? at_target : z[k];
-        }
-        if (row < g.n) {
+                z[k] = exp2_fast(fmaf(z[k], kLog2e, base));
+            if (c + q + 32 > cols || any_dead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint4 o;
-                o.x = pack2<kBf16>(z[8 * k], z[8 * k + 1]);
-                o.y = pack2<kBf16>(z[8 * k + 2], z[8 * k + 3]);
-                o.z = pack2<kBf16>(z[8 * k + 4], z[8 * k + 5]);
-                o.w = pack2<kBf16>(z[8 * k + 6], z[8 * k + 7]);
-                *reinterpret_cast<uint4*>(out + c + 8 * k) = o;
+                for (int k = 0; k < 32; ++k)
+                    z[k] = live && c + q + k < cols ? z[k] : 0.0f;
             }
+            if (__any_sync(0xffffffffu, hit >= c + q && hit < c + q + 32)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    z[k] = c + q + k == hit ? at_target : z[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                box.put(q / 8 + k, pack2<kBf16>(z[8 * k], z[8 * k + 1]), pack2<kBf16>(z[8 * k + 2], z[8 * k + 3]),
+                        pack2<kBf16>(z[8 * k + 4], z[8 * k + 5]), pack2<kBf16>(z[8 * k + 6], z[8 * k + 7]));
+        }
+        box.close();
+        if (box.first) {
+            if (c < cols && row0 < g.n)
+                tma_store(&g.out[0], box.at, col0 + c, row0);
+            store_commit();
         }
     }
 }
 
-// 128 columns of dH's binary32 sums (d is a multiple of 8).
-__device__ __forceinline__ void rows_dh(const GemmArgs& g, int split, int col0, uint32_t tmem, int row)
+// 128 columns of dH's binary32 sums.
+__device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* out, int split, int col0, int row0,
+                                        uint32_t tmem, const Box& box)
 {
-    float* out = g.dh + ((int64_t)split * g.n + row) * g.d + col0;
-    uint32_t r[32];
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 32) {
         if (col0 + c >= g.d)
             break;
-        __syncwarp();
+        box.open();
+        uint32_t r[32];
         tmem_load32(tmem + c, r);
         tmem_wait_load(r);
-        const float* z = reinterpret_cast<const float*>(r);
-        if (row < g.n) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                if (col0 + c + k < g.d) {
-                    float4 o = make_float4(z[k], z[k + 1], z[k + 2], z[k + 3]);
-                    float4* to = reinterpret_cast<float4*>(out + c + k);
-                    if (g.add) {
-                        const float4 old = *to;
-                        o.x += old.x;
-                        o.y += old.y;
-                        o.z += old.z;
-                        o.w += old.w;
-                    }
-                    *to = o;
-                }
-            }
+        for (int k = 0; k < 8; ++k)
+            box.put(k, r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        box.close();
+        if (box.first && row0 < g.n) {
+            if (g.add)
+                tma_store3<true>(out, box.at, col0 + c, row0, split);
+            else
+                tma_store3<false>(out, box.at, col0 + c, row0, split);
+            store_commit();
         }
     }
 }
 
 // 128 columns of dW, final.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dw(const GemmArgs& g, int col0, uint32_t tmem, int row)
+__device__ __forceinline__ void rows_dw(const GemmArgs& g, const CUtensorMap* out, int col0, int row0, uint32_t tmem,
+                                        const Box& box)
 {
     const float scale = *g.gscale;
-    uint16_t* out = g.dw + (int64_t)row * g.dw_ld + col0;
-    uint32_t r[32];
+    const int row = row0 + box.row;
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
+    for (int c = 0; c < kHalf; c += 64) {
         if (col0 + c >= g.d)
             break;
-        __syncwarp();
-        tmem_load32(tmem + c, r);
-        tmem_wait_load(r);
-        const float* z = reinterpret_cast<const float*>(r);
-        if (row < g.dw_rows) {
+        if (g.dw_wide)
+            box.open();
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                if (col0 + c + k < g.d) {
-                    uint32_t o[4];
+        for (int q = 0; q < 64; q += 32) {
+            uint32_t r[32];
+            tmem_load32(tmem + c + q, r);
+            tmem_wait_load(r);
+            const float* z = reinterpret_cast<const float*>(r);
+            uint32_t o[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = pack2<kBf16>(z[k + 2 * e] * scale, z[k + 2 * e + 1] * scale);
-                    if (g.dw_wide) {
-                        *reinterpret_cast<uint4*>(out + c + k) = make_uint4(o[0], o[1], o[2], o[3]);
-                    } else {
+            for (int e = 0; e < 16; ++e)
+                o[e] = pack2<kBf16>(z[2 * e] * scale, z[2 * e + 1] * scale);
+            if (g.dw_wide) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            out[c + k + 2 * e] = (uint16_t)(o[e] & 0xFFFFu);
-                            out[c + k + 2 * e + 1] = (uint16_t)(o[e] >> 16);
-                        }
+                for (int k = 0; k < 4; ++k)
+                    box.put(q / 8 + k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            } else if (row < g.dw_rows) {
+                uint16_t* to = g.dw + (int64_t)row * g.dw_ld + col0 + c + q;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (col0 + c + q + 2 * e < g.d) {
+                        to[2 * e] = (uint16_t)(o[e] & 0xFFFFu);
+                        to[2 * e + 1] = (uint16_t)(o[e] >> 16);
                     }
                 }
+            }
+            __syncwarp();
+        }
+        if (g.dw_wide) {
+            box.close();
+            if (box.first && row0 < g.dw_rows) {
+                tma_store(out, box.at, col0 + c, row0);
+                store_commit();
             }
         }
     }
@@ -335,11 +397,11 @@ template <bool kValue> struct Flag {
 // f(A is MN-major, B is MN-major) of the job: logits are rows times rows, dH
 // is dz's rows times W's columns, dW dz's columns times H's columns.
 template <int kMode, class F>
-__device__ __forceinline__ void by_layout(int job, F&& f)
+__device__ __forceinline__ void by_layout(bool dw, F&& f)
 {
     if constexpr (kMode != kGrad)
         f(Flag<false>{}, Flag<false>{});
-    else if (job == 0)
+    else if (!dw)
         f(Flag<false>{}, Flag<true>{});
     else
         f(Flag<true>{}, Flag<true>{});
@@ -393,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         uint32_t steps = 0;
         bool ok = true;
         const bool one = elect_one();
-        for (int t = worker; ok && t < g.tiles; t += workers) {
+        for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
             const Tile u = tile_at(g, t);
             const CUtensorMap* ma = &g.a[u.job];
             const CUtensorMap* mb = &g.b[u.job];
@@ -401,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             const int col0 = u.n * kTileN + (int)rank * kHalf;
             auto run = [&](auto a_mn, auto b_mn) {
                 for (int kb = u.kb0; kb < u.kb1; ++kb, ++steps, ring.next()) {
-                    if (!(ok = mbar_wait(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead)))
+                    if (!(ok = mbar_wait_warp(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead)))
                         break;
                     if (one) {
                         uint32_t full = smem_addr(s_full) + ring.at * 8;
@@ -436,11 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     __syncwarp();
                 }
             };
-            by_layout<kMode>(u.job, run);
+            by_layout<kMode>(g.job[u.job].is_dw, run);
         }
         // the last products' signals must find this block's barriers
         for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; ok && b < steps; ++b)
-            ok = mbar_wait(smem_addr(s_empty) + (b % S::kStages) * 8, (b / S::kStages) & 1, dead);
+            ok = mbar_wait_warp(smem_addr(s_empty) + (b % S::kStages) * 8, (b / S::kStages) & 1, dead);
         if (!ok && rank == 0) {  // let the loads in flight land before the block leaves
             for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; b < steps; ++b)
                 mbar_wait(smem_addr(s_full) + (b % S::kStages) * 8, (b / S::kStages) & 1, nullptr);
@@ -451,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         uint32_t acc = 0;
         bool ok = true;
         const bool one = elect_one();
-        for (int t = worker; ok && t < g.tiles; t += workers) {
+        for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
             const Tile u = tile_at(g, t);
             const uint32_t idesc = g.job[u.job].idesc;
             auto run = [&](auto a_mn, auto b_mn) {
@@ -461,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 const uint64_t desc_b = smem_desc(tiles_at + kBytesA, kBlock, 1024);
                 for (int kb = u.kb0; ok && kb < u.kb1; ++acc) {
                     const uint32_t buf = acc & 1;
-                    if (!(ok = mbar_wait(smem_addr(s_acc_empty) + buf * 8, ((acc >> 1) & 1) ^ 1, dead)))
+                    if (!(ok = mbar_wait_warp(smem_addr(s_acc_empty) + buf * 8, ((acc >> 1) & 1) ^ 1, dead)))
                         break;
                     fence_after_sync();
                     const uint32_t d = tmem + buf * kTileN;
@@ -471,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     // this step's products are issued
                     bool there = mbar_try(smem_addr(s_full) + ring.at * 8, ring.phase);
                     for (; kb < last; ++kb) {
-                        if (!there && !(ok = mbar_wait(smem_addr(s_full) + ring.at * 8, ring.phase, dead)))
+                        if (!__all_sync(0xffffffffu, there) &&
+                            !(ok = mbar_wait_warp(smem_addr(s_full) + ring.at * 8, ring.phase, dead)))
                             break;
                         fence_after_sync();
                         const uint32_t here = ring.at;
@@ -495,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     __syncwarp();
                 }
             };
-            by_layout<kMode>(u.job, run);
+            by_layout<kMode>(g.job[u.job].is_dw, run);
         }
         if (!ok) {  // let the products in flight end before tensor memory is freed
             if (one)
@@ -506,12 +569,20 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         // ---- results
         const int quad = warp & 3;  // a warp reads the 32 lanes of its quarter
         const int half = warp >> 2;
+        Box box;
+        box.row = quad * 32 + lane;
+        box.half = half;
+        box.at = tiles_at + S::kStages * S::kStageBytes + half * kOutBytes;
+        box.row_at = box.at + box.row * 128;
+        box.first = box.row == 0;
         const uint32_t lanes_at = tmem + ((uint32_t)(quad * 32) << 16) + half * kHalf;
         uint32_t acc = 0;
         bool ok = true;
         auto await = [&]() {
-            const bool mine = mbar_wait(smem_addr(&s_acc_full[acc & 1]), (acc >> 1) & 1, dead);
-            ok = __all_sync(0xffffffffu, mine);
+            // one answer in all warps that meet at the barriers of a box
+            ok = mbar_wait_warp(smem_addr(&s_acc_full[acc & 1]), (acc >> 1) & 1, dead);
+            if constexpr (kMode != kLoss)
+                ok = named_all(1 + half, 32 * kResultWarps / 2, ok);
             fence_after_sync();
             return ok;
         };
@@ -527,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             }
             ++acc;
         };
-        for (int t = worker; ok && t < g.tiles; t += workers) {
+        for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
             const Tile u = tile_at(g, t);
-            const int row = u.m * S::kTileM + (int)rank * kRows + quad * 32 + lane;
+            const int row0 = u.m * S::kTileM + (int)rank * kRows;
             const int col0 = u.n * kTileN + half * kHalf;
             if constexpr (kMode == kLoss) {
                 float z[kHalf];
@@ -552,21 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     give_back();
                 }
                 if (ok)
-                    rows_loss(g, col0, row, z);
+                    rows_loss(g, col0, row0 + quad * 32 + lane, z);
             } else {
                 if (!await())
                     break;
                 const uint32_t at = lanes_at + (acc & 1) * kTileN;
                 if constexpr (kMode == kDz)
-                    rows_dz<kBf16>(g, col0, at, row);
-                else if (u.job == 0)
-                    rows_dh(g, u.split, col0, at, row);
+                    rows_dz<kBf16>(g, col0, row0, at, box);
+                else if (!g.job[u.job].is_dw)
+                    rows_dh(g, &g.out[u.job], u.split, col0, row0, at, box);
                 else
-                    rows_dw<kBf16>(g, col0, at, row);
+                    rows_dw<kBf16>(g, &g.out[u.job], col0, row0, at, box);
                 give_back();
             }
         }
     }
+    if (kMode != kLoss && warp < kResultWarps)
+        store_wait();
     __syncwarp();
     fence_before_sync();
     __syncthreads();
@@ -917,24 +990,32 @@ EncodeFn encode_fn()
     return reinterpret_cast<EncodeFn>(f);
 }
 
-// A row-major matrix of 16-bit values, cut into boxes of 64 columns; what lies
-// outside reads as zero.
-bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+// [planes] of a row-major matrix, cut into boxes of 128 bytes by box_rows; what
+// lies outside reads as zero and is not written.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t planes, int64_t rows, int64_t cols,
+              int64_t ld, int box_rows)
 {
     EncodeFn f = encode_fn();
     if (!f)
         return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-    const cuuint32_t step[2] = {1, 1};
-    return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(p),
-             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const int64_t width = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * width), (cuuint64_t)(rows * ld * width)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / width), (cuuint32_t)box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return f(m, type, planes ? 3 : 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    return make_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 0, rows, cols, ld,
+                    box_rows);
 }
 
 template <bool kPair, int kMode, bool kBf16>
-cudaError_t launch_shape(const GemmArgs& g, cudaStream_t st)
+cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
 {
     using S = Shape<kPair>;
     const cudaError_t e = cudaFuncSetAttribute(xent_product_kernel<kPair, kMode, kBf16>,
@@ -942,7 +1023,12 @@ cudaError_t launch_shape(const GemmArgs& g, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)std::min(g.tiles * S::kCtas, kMaxCtas));
+    const int32_t tiles = g.job[0].tiles + g.job[1].tiles;
+    const int32_t workers = std::min(tiles, kMaxCtas / S::kCtas);
+    g.late = g.job[0].tiles % workers;
+    g.ahead = g.late && g.job[1].tiles
+                  ? (int32_t)std::llround((double)g.job[0].kb / g.job[0].splits * g.job[1].splits / g.job[1].kb) : 0;
+    lc.gridDim = dim3((unsigned)(workers * S::kCtas));
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = S::kSmem;
     lc.stream = st;
@@ -957,18 +1043,20 @@ cudaError_t launch_shape(const GemmArgs& g, cudaStream_t st)
 }
 
 template <int kMode, bool kBf16>
-cudaError_t launch_product(bool pair, const GemmArgs& g, cudaStream_t st)
+cudaError_t launch_product(bool pair, GemmArgs& g, cudaStream_t st)
 {
     return pair ? launch_shape<true, kMode, kBf16>(g, st) : launch_shape<false, kMode, kBf16>(g, st);
 }
 
-void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn)
+void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn,
+             int64_t band)
 {
     const int rows = pair ? 2 * kRows : kRows;
     j.mt = (int32_t)ceil_div(m, rows);
     j.nt = (int32_t)ceil_div(n, kTileN);
     j.kb = (int32_t)ceil_div(k, kTileK);
     j.splits = (int32_t)std::min<int64_t>(splits, j.kb);
+    j.band = (int32_t)std::min<int64_t>(band, j.mt);
     j.idesc = mma_desc(bf16, a_mn, b_mn, rows, kTileN);
     j.tiles = j.mt * j.nt * j.splits;
 }
@@ -982,6 +1070,10 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     float* lse = a.lse ? a.lse : reinterpret_cast<float*>(ws + p.off_lse);
     const int exponent = kBf16 ? 0 : 15;
     const bool pair = a.n > kRows;
+    // logits: up to 32 MB of hidden stay in L2 while the vocabulary streams by;
+    // gradients: one row of tiles reads its part of dz once, and the whole
+    // width of the other operand from L2
+    const int64_t band = std::max<int64_t>(1, (32ll << 20) / (a.d * 2 * (pair ? 2 * kRows : kRows)));
 
     GemmArgs g{};
     g.n = (int32_t)a.n;
@@ -1010,14 +1102,13 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     f.parts = reinterpret_cast<MergePart*>(ws + p.off_merge);
 
     if (a.n > 0) {
-        set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false);
-        g.tiles = g.job[0].tiles;
+        set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false, band);
         if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows) ||
             !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, kHalf))
             return MPT_ERR_CUDA;
         if (launch_product<kLoss, kBf16>(pair, g, st) != cudaSuccess)
             return MPT_ERR_CUDA;
-        f.nstatus = std::min(g.tiles * (pair ? 2 : 1), kMaxCtas);
+        f.nstatus = pair ? 2 * std::min(g.job[0].tiles, kMaxCtas / 2) : std::min(g.job[0].tiles, kMaxCtas);
         const MergeArgs m{static_cast<const uint16_t*>(a.hidden), static_cast<const uint16_t*>(a.weight), a.ld_hidden,
                           a.ld_weight, token, lse, const_cast<MergePart*>(f.parts)};
         xent_merge_kernel<kBf16><<<(unsigned)p.merges, kMergeRows * 32, 0, st>>>(g, m);
@@ -1037,52 +1128,53 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
 
     uint16_t* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
     auto wide = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
+    float* dh = reinterpret_cast<float*>(ws + p.off_dh);
     GemmArgs z = g;
-    z.dz = dz;
-    z.dz_ld = p.piece;
     GemmArgs q = g;
-    q.dh = reinterpret_cast<float*>(ws + p.off_dh);
     q.dw_ld = a.ld_grad_weight;
     q.dw_wide = wide(a.grad_weight, a.ld_grad_weight);
     const uint16_t* w = static_cast<const uint16_t*>(a.weight);
-    int32_t splits = 1;
+    const int32_t splits = p.want_dh ? (int32_t)std::min(p.splits, ceil_div(std::min(p.piece, a.v), kTileK)) : 0;
     for (int64_t c0 = 0; c0 < a.v; c0 += p.piece) {
         const int64_t cols = std::min(p.piece, a.v - c0);
         const uint16_t* wp = w + c0 * a.ld_weight;
         z.col0 = (int32_t)c0;
-        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false);
-        z.tiles = z.job[0].tiles;
-        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kHalf))
+        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band);
+        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kHalf) ||
+            !make_map(&z.out[0], kBf16, dz, a.n, cols, p.piece, kRows))
             return MPT_ERR_CUDA;
         if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
             return MPT_ERR_CUDA;
 
-        // columns beyond `cols` up to the tile's end are zeros in dz
         q.job[0] = q.job[1] = Job{};
+        // the job of the longer tiles comes first
+        const int64_t kb_h = p.want_dh ? ceil_div(ceil_div(cols, kTileK), splits) : 0;
+        const int at_h = kb_h >= ceil_div(a.n, kTileK) || !p.want_dw ? 0 : 1, at_w = p.want_dh ? 1 - at_h : 0;
         if (p.want_dh) {
-            set_job(q.job[0], pair, kBf16, a.n, a.d, cols, p.splits, false, true);
             // (a short last piece may add to the first sums only)
-            splits = std::max(splits, q.job[0].splits);
-            if (!make_map(&q.a[0], kBf16, dz, a.n, cols, p.piece, kRows) ||
-                !make_map(&q.b[0], kBf16, wp, cols, a.d, a.ld_weight, kTileK))
-                return MPT_ERR_CUDA;
+            set_job(q.job[at_h], pair, kBf16, a.n, a.d, cols, splits, false, true, 1);
             q.add = c0 > 0;
+            if (!make_map(&q.a[at_h], kBf16, dz, a.n, cols, p.piece, kRows) ||
+                !make_map(&q.b[at_h], kBf16, wp, cols, a.d, a.ld_weight, kTileK) ||
+                !make_map(&q.out[at_h], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dh, splits, a.n, a.d, a.d, kRows))
+                return MPT_ERR_CUDA;
         }
         if (p.want_dw) {
-            set_job(q.job[1], pair, kBf16, cols, a.d, a.n, 1, true, true);
-            if (!make_map(&q.a[1], kBf16, dz, a.n, cols, p.piece, kTileK) ||
-                !make_map(&q.b[1], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK))
-                return MPT_ERR_CUDA;
+            set_job(q.job[at_w], pair, kBf16, cols, a.d, a.n, 1, true, true, 1);
+            q.job[at_w].is_dw = 1;
             q.dw = static_cast<uint16_t*>(a.grad_weight) + c0 * a.ld_grad_weight;
             q.dw_rows = (int32_t)cols;
+            if (!make_map(&q.a[at_w], kBf16, dz, a.n, cols, p.piece, kTileK) ||
+                !make_map(&q.b[at_w], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK) ||
+                (q.dw_wide && !make_map(&q.out[at_w], kBf16, q.dw, cols, a.d, a.ld_grad_weight, kRows)))
+                return MPT_ERR_CUDA;
         }
-        q.tiles = q.job[0].tiles + q.job[1].tiles;
         if (launch_product<kGrad, kBf16>(pair, q, st) != cudaSuccess)
             return MPT_ERR_CUDA;
     }
     if (p.want_dh) {
         const int64_t blocks = std::min<int64_t>(ceil_div(a.n * (a.d / 8), 256), 148 * 8);
-        xent_dh_kernel<kBf16><<<(unsigned)blocks, 256, 0, st>>>(q.dh, splits, a.n, (int32_t)a.d, gscale,
+        xent_dh_kernel<kBf16><<<(unsigned)blocks, 256, 0, st>>>(dh, splits, a.n, (int32_t)a.d, gscale,
                                                                 static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden,
                                                                 wide(a.grad_hidden, a.ld_grad_hidden));
         if (cudaGetLastError() != cudaSuccess)

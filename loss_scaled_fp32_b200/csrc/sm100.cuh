@@ -86,6 +86,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
+// The same by a whole warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* dead)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, dead));
+}
+
 // ---- pairs of CTAs (clusters of two) ----------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -133,6 +139,56 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
     asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst), "l"(m), "r"(bar), "r"(x), "r"(y)
                  : "memory");
+}
+
+// Stores from shared memory (kAdd: binary32 sums added in L2); what lies
+// outside the tensor is not written.
+__device__ __forceinline__ void tma_store(const CUtensorMap* m, uint32_t src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(src),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
+template <bool kAdd>
+__device__ __forceinline__ void tma_store3(const CUtensorMap* m, uint32_t src, int x, int y, int z)
+{
+    if constexpr (kAdd)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
+                     "r"(src), "r"(x), "r"(y), "r"(z)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m), "r"(src),
+                     "r"(x), "r"(y), "r"(z)
+                     : "memory");
+}
+
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// the sources may be written again
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// writes to shared memory become visible to TMA
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same barrier; true if `mine` is in all of its threads.
+__device__ __forceinline__ bool named_all(int id, int threads, bool mine)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all)
+                 : "r"(id), "r"(threads), "r"(mine ? 1u : 0u)
+                 : "memory");
+    return all != 0;
+}
+
+__device__ __forceinline__ void shared_store16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // ---- tensor memory ---------------------------------------------------------
