@@ -14,6 +14,7 @@ cannot be loaded (or built with nvcc), importing the library fails loudly.
                    weight_decay=1e-4, clip=1.0)
 """
 import collections
+import contextlib
 import ctypes
 import os
 
@@ -208,8 +209,19 @@ def shard_len(total, world):
 
 def _stream_ptr(stream, device):
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the raw handle: current_stream() builds a Stream object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on(device, stream):
+    """A context in which ``device`` (and ``stream``, if given) are current."""
+    import torch
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch._C._cuda_getDevice() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 class MPT:
@@ -371,11 +383,10 @@ class MPT:
 
 
 def _type_code(dtype):
-    import torch
-    codes = {torch.float16: MPT_F16, torch.bfloat16: MPT_BF16, torch.float32: MPT_F32}
-    if dtype not in codes:
+    code = {"torch.float16": MPT_F16, "torch.bfloat16": MPT_BF16, "torch.float32": MPT_F32}.get(str(dtype))
+    if code is None:
         raise ValueError(f"{dtype} is not float16, bfloat16 or float32")
-    return codes[dtype]
+    return code
 
 
 def _scale_args(scale, device):
@@ -462,9 +473,8 @@ class GradList:
     def norm(self, grads, scale=1.0, clip=0.0, tensor_norms=False, stream=None):
         """Queue the norm of ``grads`` (CUDA tensors, or an array from
         :func:`grad_pointers`); ``clip`` only sets the ``coef`` reported."""
-        import torch
         host, dev = _scale_args(scale, self.device)
-        with torch.cuda.device(self.device):
+        with _on(self.device, stream):
             _check(lib().mpt_list_norm(self._h, self._ptrs(grads, self.dtypes, "gradient"), host, dev, clip,
                                        MPT_LIST_TENSOR_NORMS if tensor_norms else 0,
                                        _stream_ptr(stream, self.device)), "mpt_list_norm")
@@ -473,14 +483,13 @@ class GradList:
     def clip(self, grads, clip, out=None, scale=1.0, unscale=False, tensor_norms=False, stream=None):
         """Queue the norm and the scaling of ``grads`` to a norm of at most
         ``clip``, into ``out`` (default: in place)."""
-        import torch
         host, dev = _scale_args(scale, self.device)
         g = self._ptrs(grads, self.dtypes, "gradient")
         if out is None and self.out_dtypes != self.dtypes:
             raise ValueError("outputs of another type need tensors of their own")
         o = g if out is None else self._ptrs(out, self.out_dtypes, "output")
         flags = (MPT_LIST_TENSOR_NORMS if tensor_norms else 0) | (MPT_LIST_UNSCALE if unscale else 0)
-        with torch.cuda.device(self.device):
+        with _on(self.device, stream):
             _check(lib().mpt_list_clip(self._h, g, o, host, dev, clip, flags,
                                        _stream_ptr(stream, self.device)), "mpt_list_clip")
         return self._views(tensor_norms)
@@ -510,25 +519,30 @@ XentGrad = collections.namedtuple("XentGrad", "loss token_loss lse n_valid grad_
 
 def _rows(t, what, like=None):
     """The row distance of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a 2-D CUDA tensor with contiguous rows")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor")
+    n, d = t.shape
+    ld, step = t.stride()
+    if step != 1 and d > 1:
+        raise ValueError(f"{what} must have contiguous rows")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{what} must have the type and device of hidden")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+    return ld if n > 1 else max(ld, (d + 7) // 8 * 8)
 
 
 def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, grad_weight, stream):
     import torch
+    L = lib()
     a = XentArgs()
-    lib().mpt_xent_args_init(ctypes.byref(a))
+    L.mpt_xent_args_init(ctypes.byref(a))
     a.ld_hidden, a.ld_weight = _rows(hidden, "hidden"), _rows(weight, "weight", hidden)
     a.type = _type_code(hidden.dtype)
-    a.n, a.d = hidden.shape
+    n, d = a.n, a.d = hidden.shape
     a.v = weight.shape[0]
     dev = hidden.device
-    if weight.shape[1] != a.d:
+    if weight.shape[1] != d:
         raise ValueError("hidden and weight must have rows of one width")
-    if targets.shape != (a.n,) or targets.device != dev or not targets.is_contiguous() or \
+    if targets.shape != (n,) or targets.device != dev or not targets.is_contiguous() or \
             targets.dtype not in (torch.int32, torch.int64):
         raise ValueError("targets must be one int32 or int64 per row of hidden, contiguous, on its device")
     if reduction not in ("mean", "sum"):
@@ -538,31 +552,32 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
     a.reduction = MPT_XENT_SUM if reduction == "sum" else MPT_XENT_MEAN
     a.scale, a.d_scale = _scale_args(scale, dev)
     a.hidden, a.weight, a.targets = hidden.data_ptr(), weight.data_ptr(), targets.data_ptr()
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
     # what the call allocates belongs to the stream that it runs on
-    with torch.cuda.device(dev), torch.cuda.stream(s):
-        out = torch.empty(2 * a.n + 4, dtype=torch.float32, device=dev)
-        n_valid = out[:2].view(torch.int64)
-        loss, token_loss, lse = out[2:3], out[4:4 + a.n], out[4 + a.n:]
-        grads = []
-        for given, like, name in ((grad_hidden, hidden, "grad_hidden"), (grad_weight, weight, "grad_weight")):
-            if given is True:
-                given = torch.empty(like.shape, dtype=like.dtype, device=dev)
-            elif given is False or given is None:
-                given = None
-            elif given.shape != like.shape:
-                raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
-            if given is not None:
-                setattr(a, "ld_" + name, _rows(given, name, hidden))
-                setattr(a, name, given.data_ptr())
-            grads.append(given)
-        a.loss, a.token_loss, a.lse, a.n_valid = (t.data_ptr() for t in (loss, token_loss, lse, n_valid))
+    with _on(dev, stream):
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        n_valid = torch.empty(1, dtype=torch.int64, device=dev)
+        token_loss = torch.empty(n, dtype=torch.float32, device=dev)
+        lse = torch.empty(n, dtype=torch.float32, device=dev)
+        if grad_hidden is not None and grad_hidden is not False:
+            if grad_hidden is True:
+                grad_hidden = torch.empty((n, d), dtype=hidden.dtype, device=dev)
+            elif grad_hidden.shape != hidden.shape:
+                raise ValueError(f"grad_hidden must have the shape {tuple(hidden.shape)}")
+            a.ld_grad_hidden, a.grad_hidden = _rows(grad_hidden, "grad_hidden", hidden), grad_hidden.data_ptr()
+        if grad_weight is not None and grad_weight is not False:
+            if grad_weight is True:
+                grad_weight = torch.empty((a.v, d), dtype=hidden.dtype, device=dev)
+            elif grad_weight.shape != weight.shape:
+                raise ValueError(f"grad_weight must have the shape {tuple(weight.shape)}")
+            a.ld_grad_weight, a.grad_weight = _rows(grad_weight, "grad_weight", hidden), grad_weight.data_ptr()
+        a.loss, a.n_valid = loss.data_ptr(), n_valid.data_ptr()
+        a.token_loss, a.lse = token_loss.data_ptr(), lse.data_ptr()
         nbytes = ctypes.c_size_t()
-        _check(lib().mpt_xent_workspace_bytes(ctypes.byref(a), ctypes.byref(nbytes)), "mpt_xent_workspace_bytes")
+        _check(L.mpt_xent_workspace_bytes(ctypes.byref(a), ctypes.byref(nbytes)), "mpt_xent_workspace_bytes")
         ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
-        _check(lib().mpt_xent(ctypes.byref(a), ctypes.c_void_p(ws.data_ptr()), nbytes.value,
-                              ctypes.c_void_p(s.cuda_stream)), "mpt_xent")
-    return loss, token_loss, lse, n_valid, grads[0], grads[1]
+        _check(L.mpt_xent(ctypes.byref(a), ws.data_ptr(), nbytes.value, _stream_ptr(stream, dev)), "mpt_xent")
+    return loss, token_loss, lse, n_valid, None if grad_hidden is False else grad_hidden, \
+        None if grad_weight is False else grad_weight
 
 
 def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stream=None):

@@ -39,6 +39,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
 constexpr int kGranule = 512;      // bytes: one 16-byte load per lane
 constexpr int kPtrSlots = 4;       // pointer tables held on the device at once
+constexpr int kLongRuns = 128;
 constexpr size_t kAlign = 256;
 
 // What one warp's share holds of one tensor.
@@ -61,6 +62,7 @@ struct ListArgs {
     const Run* runs;
     const int32_t* warp_runs;       // first run of every warp, and the end
     const int32_t* tensor_runs;     // first run of every tensor, and the end
+    const int32_t* long_tensors;    // tensors of more than kLongRuns runs
     const void* const* grads;
     void* const* outs;              // clip only
     double* run_sums;
@@ -71,6 +73,7 @@ struct ListArgs {
     float scale;                    // S from the host
     float clip;
     int32_t n;
+    int32_t n_long;
     int32_t sum_ctas;               // CTAs of the norm pass
     int32_t want_tensor_norms;
     int32_t unscale;
@@ -317,15 +320,43 @@ __device__ __forceinline__ void write_result(const ListArgs& a, const Totals& t)
     *a.result = r;
 }
 
-// One warp per tensor, over the whole grid.
+// One warp per tensor, over the whole grid; the few tensors of many runs one
+// CTA each (a single warp took 12 us for the 4096 runs of a million values).
 __device__ __forceinline__ void write_tensor_norms(const ListArgs& a)
 {
-    const int lane = threadIdx.x & 31;
+    __shared__ double s_part[kWarps];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const double S = (double)(a.d_scale ? *a.d_scale : a.scale);
-    for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < a.n; i += gridDim.x * kWarps) {
-        const int end = a.tensor_runs[i + 1];
+    for (int k = blockIdx.x; k < a.n_long; k += gridDim.x) {
+        const int i = a.long_tensors[k];
+        const int first = a.tensor_runs[i], end = a.tensor_runs[i + 1];
         double s = 0.0;
-        for (int r = a.tensor_runs[i] + lane; r < end; r += 32)
+        for (int r = first + threadIdx.x; r < end; r += 4 * kThreads) {
+            double q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = r + e * kThreads < end ? __ldcg(a.run_sums + r + e * kThreads) : 0.0;
+            s += (q[0] + q[1]) + (q[2] + q[3]);
+        }
+        s = warp_sum(s);
+        if (lane == 0)
+            s_part[w] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double t = 0.0;
+#pragma unroll
+            for (int e = 0; e < kWarps; ++e)
+                t += s_part[e];
+            a.tensor_norms[i] = sqrt(t) / S;
+        }
+        __syncthreads();
+    }
+    for (int i = blockIdx.x * kWarps + w; i < a.n; i += gridDim.x * kWarps) {
+        const int first = a.tensor_runs[i], end = a.tensor_runs[i + 1];
+        if (end - first > kLongRuns)
+            continue;
+        double s = 0.0;
+        for (int r = first + lane; r < end; r += 32)
             s += __ldcg(a.run_sums + r);
         s = warp_sum(s);
         if (lane == 0)
@@ -500,9 +531,10 @@ struct Plan {
     std::vector<Run> runs;
     std::vector<int32_t> warp_runs;
     std::vector<int32_t> tensor_runs;
+    std::vector<int32_t> long_tensors;
     int32_t ctas = 0;
     size_t off_result = 0, off_norms = 0, off_cta = 0, off_run_sums = 0, off_ptrs = 0, off_runs = 0,
-           off_warp = 0, off_tensor = 0, total = 0;
+           off_warp = 0, off_tensor = 0, off_long = 0, total = 0;
 };
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -555,6 +587,8 @@ int build_plan(const int64_t* sizes, const int32_t* types, const int32_t* out_ty
             at += r.len;
             done += take;
         }
+        if ((int64_t)p.runs.size() - p.tensor_runs.back() > kLongRuns)
+            p.long_tensors.push_back(i);
         p.tensor_runs.push_back((int32_t)p.runs.size());
     }
     while ((int64_t)p.warp_runs.size() < warps + 1)
@@ -574,6 +608,7 @@ int build_plan(const int64_t* sizes, const int32_t* types, const int32_t* out_ty
     p.off_runs = region(sizeof(Run) * p.runs.size());
     p.off_warp = region(sizeof(int32_t) * p.warp_runs.size());
     p.off_tensor = region(sizeof(int32_t) * p.tensor_runs.size());
+    p.off_long = region(sizeof(int32_t) * p.long_tensors.size());
     p.total = at;
     return MPT_OK;
 }
@@ -799,6 +834,8 @@ int enqueue(mpt_list* h, const void* const* grads, void* const* outs, float scal
     a.d_scale = d_scale;
     a.scale = scale;
     a.clip = clip;
+    a.long_tensors = reinterpret_cast<const int32_t*>(h->ws + p.off_long);
+    a.n_long = (int32_t)p.long_tensors.size();
     a.n = h->n;
     a.sum_ctas = p.ctas;
     a.want_tensor_norms = (flags & MPT_LIST_TENSOR_NORMS) ? 1 : 0;
@@ -810,7 +847,7 @@ int enqueue(mpt_list* h, const void* const* grads, void* const* outs, float scal
     if (outs) {
         e = launch(list_clip_kernel, p.ctas, true, a, st);
     } else {
-        const int grid = a.want_tensor_norms ? std::min(148, (h->n + kWarps - 1) / kWarps) : 1;
+        const int grid = a.want_tensor_norms ? std::min(148, std::max((h->n + kWarps - 1) / kWarps, a.n_long)) : 1;
         e = launch(list_finish_kernel, grid, true, a, st);
     }
     return e == cudaSuccess ? MPT_OK : fail_cuda(h);
@@ -890,6 +927,7 @@ int mpt_list_create(const int64_t* sizes, const int32_t* types, const int32_t* o
               upload(ws + p.off_runs, p.runs.data(), sizeof(Run) * p.runs.size()) &&
               upload(ws + p.off_warp, p.warp_runs.data(), sizeof(int32_t) * p.warp_runs.size()) &&
               upload(ws + p.off_tensor, p.tensor_runs.data(), sizeof(int32_t) * p.tensor_runs.size()) &&
+              upload(ws + p.off_long, p.long_tensors.data(), sizeof(int32_t) * p.long_tensors.size()) &&
               cudaMemset(ws, 0, p.off_ptrs) == cudaSuccess &&
               cudaHostAlloc(reinterpret_cast<void**>(&h->mailbox), sizeof(mpt_check_result), cudaHostAllocDefault) == cudaSuccess;
     for (auto& s : h->slot)

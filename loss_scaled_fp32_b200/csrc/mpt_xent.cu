@@ -85,6 +85,19 @@ struct Job {
     uint32_t idesc;
     int32_t tiles;
     int32_t is_dw;        // kGrad: dW (else dH)
+    // kGrad: results are final, g * sum in 16 bits (else binary32 sums)
+    int32_t final;
+    int32_t rows;
+    int32_t wide;         // TMA can store them; if not:
+    uint16_t* to;
+    int64_t ld;
+};
+
+// Start of the workspace.
+struct Control {
+    float gscale;           // S / rows, with the scaling of dz taken back
+    unsigned int ticket;    // of the merging CTAs
+    int32_t status[kMaxCtas];  // of the forward pass's CTAs: 1 after a wait that ran out
 };
 
 struct RowStats {
@@ -107,7 +120,7 @@ struct GemmArgs {
     // kLoss
     float2* part;         // [n][part_ld]: maximum and sum of 128 columns
     int32_t part_ld;
-    int32_t* status;      // one per CTA: 1 after a wait that ran out
+    Control* control;
     // kDz
     RowStats stats;
     int32_t col0;         // first column of the piece
@@ -115,11 +128,6 @@ struct GemmArgs {
     // kGrad
     int32_t d;
     int32_t add;          // dH: add to what an earlier piece left there
-    uint16_t* dw;         // rows of this piece, where TMA cannot store them
-    int64_t dw_ld;
-    int32_t dw_rows;
-    int32_t dw_wide;      // TMA can
-    const float* gscale;
     float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
 };
 
@@ -323,18 +331,18 @@ __device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* ou
     }
 }
 
-// 128 columns of dW, final.
+// 128 columns of a gradient, final.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dw(const GemmArgs& g, const CUtensorMap* out, int col0, int row0, uint32_t tmem,
-                                        const Box& box)
+__device__ __forceinline__ void rows_final(const GemmArgs& g, const Job& j, const CUtensorMap* out, int col0, int row0,
+                                           uint32_t tmem, const Box& box)
 {
-    const float scale = *g.gscale;
+    const float scale = g.control->gscale;
     const int row = row0 + box.row;
 #pragma unroll 1
     for (int c = 0; c < kHalf; c += 64) {
         if (col0 + c >= g.d)
             break;
-        if (g.dw_wide)
+        if (j.wide)
             box.open();
 #pragma unroll
         for (int q = 0; q < 64; q += 32) {
@@ -346,12 +354,12 @@ __device__ __forceinline__ void rows_dw(const GemmArgs& g, const CUtensorMap* ou
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 o[e] = pack2<kBf16>(z[2 * e] * scale, z[2 * e + 1] * scale);
-            if (g.dw_wide) {
+            if (j.wide) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     box.put(q / 8 + k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            } else if (row < g.dw_rows) {
-                uint16_t* to = g.dw + (int64_t)row * g.dw_ld + col0 + c + q;
+            } else if (row < j.rows) {
+                uint16_t* to = j.to + (int64_t)row * j.ld + col0 + c + q;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (col0 + c + q + 2 * e < g.d) {
@@ -362,9 +370,9 @@ __device__ __forceinline__ void rows_dw(const GemmArgs& g, const CUtensorMap* ou
             }
             __syncwarp();
         }
-        if (g.dw_wide) {
+        if (j.wide) {
             box.close();
-            if (box.first && row0 < g.dw_rows) {
+            if (box.first && row0 < j.rows) {
                 tma_store(out, box.at, col0 + c, row0);
                 store_commit();
             }
@@ -421,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     const uint32_t rank = kPair ? cluster_rank() : 0;
     const int worker = blockIdx.x / S::kCtas, workers = gridDim.x / S::kCtas;
 
+    let_next_start();
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(smem_addr(&s_full[s]), 1);
@@ -444,6 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     fence_after_sync();
     const uint32_t tmem = s_tmem;
     volatile int* dead = &s_dead;
+    if (kMode != kLoss)
+        wait_for_previous();
+    else if (blockIdx.x == 0 && threadIdx.x == 0)
+        g.control->ticket = 0;
 
     // The loading and the multiplying warp run their loops as whole warps, so
     // that addresses and descriptors stay in uniform registers, and one lane
@@ -630,10 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 const uint32_t at = lanes_at + (acc & 1) * kTileN;
                 if constexpr (kMode == kDz)
                     rows_dz<kBf16>(g, col0, row0, at, box);
-                else if (!g.job[u.job].is_dw)
+                else if (!g.job[u.job].final)
                     rows_dh(g, &g.out[u.job], u.split, col0, row0, at, box);
                 else
-                    rows_dw<kBf16>(g, &g.out[u.job], col0, row0, at, box);
+                    rows_final<kBf16>(g, g.job[u.job], &g.out[u.job], col0, row0, at, box);
                 give_back();
             }
         }
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         tmem_free<kPair>(tmem, 512);
     if (threadIdx.x == 0) {
         if constexpr (kMode == kLoss)
-            g.status[blockIdx.x] = s_dead;
+            g.control->status[blockIdx.x] = s_dead;
         else if (s_dead)
             *g.poison = __int_as_float(0x7fc00000);
     }
@@ -703,42 +716,69 @@ struct MergeArgs {
     int64_t ld_hidden, ld_weight;
     float* token_loss;
     float* lse;
-    MergePart* out;
+    MergePart* parts;      // one per CTA
+    int32_t nstatus;
+    int32_t mean;
+    float scale;
+    const float* d_scale;
+    float* loss;
+    int64_t* n_valid;
 };
 
+// The parts of each row (one warp) put together; the CTA that is done last
+// adds the rows' losses in a fixed order.
 template <bool kBf16>
 __global__ void __launch_bounds__(kMergeRows * 32)
-xent_merge_kernel(const __grid_constant__ GemmArgs g, MergeArgs a)
+xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ MergeArgs a)
 {
-    __shared__ float s_loss[kMergeRows];
-    __shared__ int s_valid[kMergeRows];
+    __shared__ double s_loss[kMergeRows];
+    __shared__ unsigned long long s_valid[kMergeRows];
+    __shared__ int s_last, s_bad;
+    let_next_start();
+    wait_for_previous();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * kMergeRows + w;
     float loss = 0.0f;
     bool valid = false;
     if (row < g.n) {
+        const int64_t t = target_of(g, row);
+        const bool known = t >= 0 && t < g.v;
+        valid = t != g.ignore;
+        float zt = 0.0f;
+        if (valid && known)
+            zt = target_logit<kBf16>(a.hidden + (int64_t)row * a.ld_hidden, a.weight + t * a.ld_weight, g.d, lane);
+        // maximum and sum of each lane's parts, then of the lanes'
         const float2* p = g.part + (int64_t)row * g.part_ld;
-        float top = -INFINITY;
-        for (int k = lane; k < g.part_ld; k += 32)
-            top = fmaxf(top, p[k].x);
+        float top = -INFINITY, sum = 0.0f;
+        for (int k = lane; k < g.part_ld; k += 32 * 8) {
+            float2 q[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                q[e] = k + 32 * e < g.part_ld ? __ldcg(p + k + 32 * e) : make_float2(-INFINITY, 0.0f);
+            float now = top;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                now = fmaxf(now, q[e].x);
+            const float base = now == -INFINITY ? 0.0f : now;
+            sum *= expf(top - base);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum += q[e].y * expf(q[e].x - base);
+            top = now;
+        }
+        float all = top;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        for (int k = lane; k < g.part_ld; k += 32)
-            sum += p[k].y * expf(p[k].x - base);
+            all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+        const float base = all == -INFINITY ? 0.0f : all;
+        sum *= expf(top - base);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float others = base + logf(sum);  // -inf where there are none
-        const int64_t t = target_of(g, row);
         float total = others;
-        valid = t != g.ignore;
         if (valid) {
-            if (t >= 0 && t < g.v) {
-                const float zt = target_logit<kBf16>(a.hidden + (int64_t)row * a.ld_hidden, a.weight + t * a.ld_weight,
-                                                     g.d, lane);
+            if (known) {
                 const float over = others - zt;
                 loss = fmaxf(over, 0.0f) + log1pf(expf(-fabsf(over)));
                 if (isnan(over))
@@ -754,74 +794,57 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, MergeArgs a)
         }
     }
     if (lane == 0) {
-        s_loss[w] = loss;
+        s_loss[w] = (double)loss;
         s_valid[w] = valid ? 1 : 0;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
         MergePart m{0.0, 0};
         for (int k = 0; k < kMergeRows; ++k) {
-            m.loss += (double)s_loss[k];
-            m.valid += (unsigned long long)s_valid[k];
+            m.loss += s_loss[k];
+            m.valid += s_valid[k];
         }
-        a.out[blockIdx.x] = m;
-    }
-}
-
-struct FinalArgs {
-    const MergePart* parts;
-    int32_t nparts;
-    const int32_t* status;
-    int32_t nstatus;
-    int32_t mean;
-    float scale;
-    const float* d_scale;
-    int32_t exponent;
-    float* loss;
-    int64_t* n_valid;
-    float* gscale;
-};
-
-__global__ void __launch_bounds__(256) xent_final_kernel(FinalArgs a)
-{
-    __shared__ double s_loss[8];
-    __shared__ unsigned long long s_valid[8];
-    __shared__ int s_bad;
-    if (threadIdx.x == 0)
+        a.parts[blockIdx.x] = m;
+        __threadfence();
+        s_last = atomicAdd(&g.control->ticket, 1u) == gridDim.x - 1;
         s_bad = 0;
-    __syncthreads();
-    double loss = 0.0;
-    unsigned long long valid = 0;
-    for (int k = threadIdx.x; k < a.nparts; k += 256) {
-        loss += a.parts[k].loss;
-        valid += a.parts[k].valid;
     }
-    for (int k = threadIdx.x; k < a.nstatus; k += 256)
-        if (a.status[k])
+    __syncthreads();
+    if (!s_last)
+        return;
+    __threadfence();
+    double sum = 0.0;
+    unsigned long long count = 0;
+    for (int k = threadIdx.x; k < (int)gridDim.x; k += kMergeRows * 32) {
+        sum += __ldcg(&a.parts[k].loss);
+        count += __ldcg(&a.parts[k].valid);
+    }
+    for (int k = threadIdx.x; k < a.nstatus; k += kMergeRows * 32)
+        if (g.control->status[k])
             s_bad = 1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        loss += __shfl_xor_sync(0xffffffffu, loss, o);
-        valid += __shfl_xor_sync(0xffffffffu, valid, o);
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
     }
-    if ((threadIdx.x & 31) == 0) {
-        s_loss[threadIdx.x >> 5] = loss;
-        s_valid[threadIdx.x >> 5] = valid;
+    if (lane == 0) {
+        s_loss[w] = sum;
+        s_valid[w] = count;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        loss = 0.0;
-        valid = 0;
-        for (int w = 0; w < 8; ++w) {
-            loss += s_loss[w];
-            valid += s_valid[w];
+        sum = 0.0;
+        count = 0;
+        for (int k = 0; k < kMergeRows; ++k) {
+            sum += s_loss[k];
+            count += s_valid[k];
         }
-        const double by = a.mean && valid > 0 ? (double)valid : 1.0;
-        *a.loss = s_bad ? __int_as_float(0x7fc00000) : (float)(loss / by);
+        const double by = a.mean && count > 0 ? (double)count : 1.0;
+        *a.loss = s_bad ? __int_as_float(0x7fc00000) : (float)(sum / by);
         if (a.n_valid)
-            *a.n_valid = (int64_t)valid;
+            *a.n_valid = (int64_t)count;
         const double S = (double)(a.d_scale ? *a.d_scale : a.scale);
-        *a.gscale = (float)ldexp(S / by, -a.exponent);
+        g.control->gscale = (float)ldexp(S / by, -(int)g.exponent);
     }
 }
 
@@ -831,6 +854,7 @@ __global__ void __launch_bounds__(256)
 xent_dh_kernel(const float* part, int32_t splits, int64_t n, int32_t d, const float* gscale, uint16_t* out,
                int64_t ld, int32_t wide)
 {
+    wait_for_previous();
     const int32_t per = d / 8;
     const float scale = *gscale;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * per; i += (int64_t)gridDim.x * 256) {
@@ -876,6 +900,7 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 struct Plan {
     bool grad = false, want_dh = false, want_dw = false;
+    bool dh_final = false;  // one piece, one sum: no sums in between
     int64_t parts = 0;      // 128-column parts of the whole vocabulary
     int64_t piece = 0;      // columns of one piece of the backward pass
     int64_t splits = 1;     // of dH's sums over a piece
@@ -886,6 +911,7 @@ struct Plan {
 
 // The piece: dz of one piece is at most 256 MB (and at least 2048 columns).
 constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int64_t kLeastSplit = 16;  // blocks of 64 in one part of a cut sum
 
 int make_plan(const mpt_xent_args& a, Plan& p)
 {
@@ -893,14 +919,14 @@ int make_plan(const mpt_xent_args& a, Plan& p)
     p.want_dw = a.grad_weight != nullptr;
     p.grad = p.want_dh || p.want_dw;
     p.parts = ceil_div(a.v, kHalf);
-    p.merges = ceil_div(a.n, kMergeRows);
+    p.merges = std::max<int64_t>(1, ceil_div(a.n, kMergeRows));
     size_t at = 0;
     auto region = [&](size_t bytes) {
         const size_t here = at;
         at = (size_t)round_up((int64_t)(at + bytes), kAlign);
         return here;
     };
-    p.off_ctl = region(256 + sizeof(int32_t) * kMaxCtas);
+    p.off_ctl = region(sizeof(Control));
     p.off_part = region(sizeof(float2) * (size_t)(a.n * p.parts));
     p.off_token = region(sizeof(float) * (size_t)a.n);
     p.off_lse = region(sizeof(float) * (size_t)a.n);
@@ -915,8 +941,10 @@ int make_plan(const mpt_xent_args& a, Plan& p)
             const int64_t tiles_h = ceil_div(a.n, kRows) * ceil_div(a.d, kTileN);
             const int64_t tiles_w = p.want_dw ? ceil_div(p.piece, kRows) * ceil_div(a.d, kTileN) : 0;
             const int64_t share = (tiles_h * kb_v + tiles_w * kb_n) / kMaxCtas;
-            p.splits = std::min<int64_t>(64, ceil_div(kb_v, std::max<int64_t>(8, share / 2)));
-            p.off_dh = region((size_t)(p.splits * a.n * a.d * 4));
+            p.splits = std::min<int64_t>(64, ceil_div(kb_v, std::max<int64_t>(kLeastSplit, share / 2)));
+            p.dh_final = p.splits == 1 && p.piece >= a.v;
+            if (!p.dh_final)
+                p.off_dh = region((size_t)(p.splits * a.n * a.d * 4));
         }
     }
     p.total = at;
@@ -1018,10 +1046,19 @@ template <bool kPair, int kMode, bool kBf16>
 cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
 {
     using S = Shape<kPair>;
-    const cudaError_t e = cudaFuncSetAttribute(xent_product_kernel<kPair, kMode, kBf16>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    // once per device; a failure is not remembered
+    static std::atomic<uint64_t> set_up{0};
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (!(set_up.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(xent_product_kernel<kPair, kMode, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess)
+            return e;
+        set_up.fetch_or(bit, std::memory_order_release);
+    }
     cudaLaunchConfig_t lc = {};
     const int32_t tiles = g.job[0].tiles + g.job[1].tiles;
     const int32_t workers = std::min(tiles, kMaxCtas / S::kCtas);
@@ -1032,14 +1069,31 @@ cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = S::kSmem;
     lc.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = S::kCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = kMode == kLoss ? 1 : 2;  // the first of the chain follows others' work
+    return cudaLaunchKernelEx(&lc, xent_product_kernel<kPair, kMode, kBf16>, g);
+}
+
+template <class K, class... A>
+cudaError_t launch_next(K kernel, int64_t grid, int threads, cudaStream_t st, const A&... args)
+{
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)grid);
+    lc.blockDim = dim3(threads);
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, xent_product_kernel<kPair, kMode, kBf16>, g);
+    return cudaLaunchKernelEx(&lc, kernel, args...);
 }
 
 template <int kMode, bool kBf16>
@@ -1064,11 +1118,9 @@ void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int6
 template <bool kBf16>
 int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
 {
-    float* gscale = reinterpret_cast<float*>(ws + p.off_ctl);
-    int32_t* status = reinterpret_cast<int32_t*>(ws + p.off_ctl + 256);
+    Control* control = reinterpret_cast<Control*>(ws + p.off_ctl);
     float* token = a.token_loss ? a.token_loss : reinterpret_cast<float*>(ws + p.off_token);
     float* lse = a.lse ? a.lse : reinterpret_cast<float*>(ws + p.off_lse);
-    const int exponent = kBf16 ? 0 : 15;
     const bool pair = a.n > kRows;
     // logits: up to 32 MB of hidden stay in L2 while the vocabulary streams by;
     // gradients: one row of tiles reads its part of dz once, and the whole
@@ -1084,22 +1136,24 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     g.ignore = a.ignore_index;
     g.part = reinterpret_cast<float2*>(ws + p.off_part);
     g.part_ld = (int32_t)p.parts;
-    g.status = status;
+    g.control = control;
     g.stats = {lse, token};
-    g.exponent = (float)exponent;
-    g.gscale = gscale;
+    g.exponent = kBf16 ? 0.0f : 15.0f;
     g.poison = a.loss;
 
-    FinalArgs f{};
-    f.mean = a.reduction == MPT_XENT_MEAN;
-    f.scale = a.scale;
-    f.d_scale = a.d_scale;
-    f.exponent = exponent;
-    f.loss = a.loss;
-    f.n_valid = a.n_valid;
-    f.gscale = gscale;
-    f.status = status;
-    f.parts = reinterpret_cast<MergePart*>(ws + p.off_merge);
+    MergeArgs m{};
+    m.hidden = static_cast<const uint16_t*>(a.hidden);
+    m.weight = static_cast<const uint16_t*>(a.weight);
+    m.ld_hidden = a.ld_hidden;
+    m.ld_weight = a.ld_weight;
+    m.token_loss = token;
+    m.lse = lse;
+    m.parts = reinterpret_cast<MergePart*>(ws + p.off_merge);
+    m.mean = a.reduction == MPT_XENT_MEAN;
+    m.scale = a.scale;
+    m.d_scale = a.d_scale;
+    m.loss = a.loss;
+    m.n_valid = a.n_valid;
 
     if (a.n > 0) {
         set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false, band);
@@ -1108,14 +1162,11 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
             return MPT_ERR_CUDA;
         if (launch_product<kLoss, kBf16>(pair, g, st) != cudaSuccess)
             return MPT_ERR_CUDA;
-        f.nstatus = pair ? 2 * std::min(g.job[0].tiles, kMaxCtas / 2) : std::min(g.job[0].tiles, kMaxCtas);
-        const MergeArgs m{static_cast<const uint16_t*>(a.hidden), static_cast<const uint16_t*>(a.weight), a.ld_hidden,
-                          a.ld_weight, token, lse, const_cast<MergePart*>(f.parts)};
-        xent_merge_kernel<kBf16><<<(unsigned)p.merges, kMergeRows * 32, 0, st>>>(g, m);
-        f.nparts = (int32_t)p.merges;
+        m.nstatus = pair ? 2 * std::min(g.job[0].tiles, kMaxCtas / 2) : std::min(g.job[0].tiles, kMaxCtas);
+    } else if (cudaMemsetAsync(control, 0, sizeof(Control), st) != cudaSuccess) {
+        return MPT_ERR_CUDA;
     }
-    xent_final_kernel<<<1, 256, 0, st>>>(f);
-    if (cudaGetLastError() != cudaSuccess)
+    if (launch_next(xent_merge_kernel<kBf16>, p.merges, kMergeRows * 32, st, g, m) != cudaSuccess)
         return MPT_ERR_CUDA;
     if (!p.grad)
         return MPT_OK;
@@ -1131,8 +1182,6 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     float* dh = reinterpret_cast<float*>(ws + p.off_dh);
     GemmArgs z = g;
     GemmArgs q = g;
-    q.dw_ld = a.ld_grad_weight;
-    q.dw_wide = wide(a.grad_weight, a.ld_grad_weight);
     const uint16_t* w = static_cast<const uint16_t*>(a.weight);
     const int32_t splits = p.want_dh ? (int32_t)std::min(p.splits, ceil_div(std::min(p.piece, a.v), kTileK)) : 0;
     for (int64_t c0 = 0; c0 < a.v; c0 += p.piece) {
@@ -1152,32 +1201,41 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
         const int at_h = kb_h >= ceil_div(a.n, kTileK) || !p.want_dw ? 0 : 1, at_w = p.want_dh ? 1 - at_h : 0;
         if (p.want_dh) {
             // (a short last piece may add to the first sums only)
-            set_job(q.job[at_h], pair, kBf16, a.n, a.d, cols, splits, false, true, 1);
+            Job& j = q.job[at_h];
+            set_job(j, pair, kBf16, a.n, a.d, cols, splits, false, true, 1);
             q.add = c0 > 0;
+            j.final = p.dh_final;
+            j.rows = (int32_t)a.n;
+            j.wide = wide(a.grad_hidden, a.ld_grad_hidden);
+            j.to = static_cast<uint16_t*>(a.grad_hidden);
+            j.ld = a.ld_grad_hidden;
             if (!make_map(&q.a[at_h], kBf16, dz, a.n, cols, p.piece, kRows) ||
                 !make_map(&q.b[at_h], kBf16, wp, cols, a.d, a.ld_weight, kTileK) ||
-                !make_map(&q.out[at_h], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dh, splits, a.n, a.d, a.d, kRows))
+                (!j.final && !make_map(&q.out[at_h], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dh, splits, a.n, a.d, a.d, kRows)) ||
+                (j.final && j.wide && !make_map(&q.out[at_h], kBf16, j.to, a.n, a.d, j.ld, kRows)))
                 return MPT_ERR_CUDA;
         }
         if (p.want_dw) {
-            set_job(q.job[at_w], pair, kBf16, cols, a.d, a.n, 1, true, true, 1);
-            q.job[at_w].is_dw = 1;
-            q.dw = static_cast<uint16_t*>(a.grad_weight) + c0 * a.ld_grad_weight;
-            q.dw_rows = (int32_t)cols;
+            Job& j = q.job[at_w];
+            set_job(j, pair, kBf16, cols, a.d, a.n, 1, true, true, 1);
+            j.is_dw = j.final = 1;
+            j.rows = (int32_t)cols;
+            j.wide = wide(a.grad_weight, a.ld_grad_weight);
+            j.to = static_cast<uint16_t*>(a.grad_weight) + c0 * a.ld_grad_weight;
+            j.ld = a.ld_grad_weight;
             if (!make_map(&q.a[at_w], kBf16, dz, a.n, cols, p.piece, kTileK) ||
                 !make_map(&q.b[at_w], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK) ||
-                (q.dw_wide && !make_map(&q.out[at_w], kBf16, q.dw, cols, a.d, a.ld_grad_weight, kRows)))
+                (j.wide && !make_map(&q.out[at_w], kBf16, j.to, cols, a.d, j.ld, kRows)))
                 return MPT_ERR_CUDA;
         }
         if (launch_product<kGrad, kBf16>(pair, q, st) != cudaSuccess)
             return MPT_ERR_CUDA;
     }
-    if (p.want_dh) {
+    if (p.want_dh && !p.dh_final) {
         const int64_t blocks = std::min<int64_t>(ceil_div(a.n * (a.d / 8), 256), 148 * 8);
-        xent_dh_kernel<kBf16><<<(unsigned)blocks, 256, 0, st>>>(dh, splits, a.n, (int32_t)a.d, gscale,
-                                                                static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden,
-                                                                wide(a.grad_hidden, a.ld_grad_hidden));
-        if (cudaGetLastError() != cudaSuccess)
+        if (launch_next(xent_dh_kernel<kBf16>, blocks, 256, st, (const float*)dh, splits, a.n, (int32_t)a.d,
+                        (const float*)&control->gscale, static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden,
+                        (int32_t)wide(a.grad_hidden, a.ld_grad_hidden)) != cudaSuccess)
             return MPT_ERR_CUDA;
     }
     return MPT_OK;

@@ -31,6 +31,12 @@ __device__ __forceinline__ bool elect_one()
     return pred != 0;
 }
 
+// ---- programmatic launch: the next kernel of a chain may take its place
+// early, and waits for the end of the one before it where it first needs it
+
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- mbarriers -------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
