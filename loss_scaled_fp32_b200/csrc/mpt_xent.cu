@@ -60,12 +60,14 @@ constexpr int kPromote = 512 / kTileK;
 // backward pass.)
 constexpr int kOutBytes = kRows * 128;
 
-// Shared memory of one load stage, and how many fit.
-template <bool kPair> struct Shape {
+// Shared memory of one load stage, and how many fit.  Seven stages keep
+// 224 KB of loads in flight (the forward pass stores nothing by TMA).
+template <bool kPair, int kMode> struct Shape {
     static constexpr int kBytesB = (kPair ? kTileN / 2 : kTileN) * kTileK * 2;
     static constexpr int kStageBytes = kBytesA + kBytesB;
-    static constexpr int kStages = 6 * 32768 / kStageBytes;
-    static constexpr int kSmem = kStages * kStageBytes + 2 * kOutBytes + 1024;
+    static constexpr int kOut = kMode == 0 ? 0 : 2 * kOutBytes;
+    static constexpr int kStages = (7 * 32768 - kOut) / kStageBytes;
+    static constexpr int kSmem = kStages * kStageBytes + kOut + 1024;
     static constexpr int kTileM = kPair ? 2 * kRows : kRows;
     static constexpr int kCtas = kPair ? 2 : 1;
 };
@@ -82,6 +84,7 @@ enum Mode { kLoss, kDz, kGrad };
 struct Job {
     int32_t mt, nt, splits, kb;
     int32_t band;
+    int32_t tn;           // columns of a tile: a multiple of 16, at most 256
     uint32_t idesc;
     int32_t tiles;
     int32_t is_dw;        // kGrad: dW (else dH)
@@ -118,7 +121,7 @@ struct GemmArgs {
     int32_t target_bytes;
     int64_t ignore;
     // kLoss
-    float2* part;         // [n][part_ld]: maximum and sum of 128 columns
+    float2* part;         // [n][part_ld]: maximum and sum of half a tile's columns
     int32_t part_ld;
     Control* control;
     // kDz
@@ -150,7 +153,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
 }
 
 struct Tile {
-    int job, m, n, split, kb0, kb1;
+    int job, m, n, split, kb0, kb1, tn;
 };
 
 // The k-th tile of a worker, or -1.
@@ -175,30 +178,51 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t)
     r.job = t >= g.job[0].tiles ? 1 : 0;
     const Job& j = g.job[r.job];
     int i = t - (r.job ? g.job[0].tiles : 0);
-    r.split = i / (j.mt * j.nt);
-    i -= r.split * (j.mt * j.nt);
-    const int m0 = i / (j.band * j.nt) * j.band, rows = min(j.band, j.mt - m0);
-    i -= m0 * j.nt;
-    r.n = i / rows;
-    r.m = m0 + i - r.n * rows;
-    r.kb0 = (int)((int64_t)j.kb * r.split / j.splits);
-    r.kb1 = (int)((int64_t)j.kb * (r.split + 1) / j.splits);
+    r.split = 0;
+    r.tn = j.tn;
+    if (j.splits > 1) {
+        r.split = i / (j.mt * j.nt);
+        i -= r.split * (j.mt * j.nt);
+    }
+    if (j.band == 1) {
+        r.m = i / j.nt;
+        r.n = i - r.m * j.nt;
+    } else {
+        const int m0 = i / (j.band * j.nt) * j.band, rows = min(j.band, j.mt - m0);
+        i -= m0 * j.nt;
+        r.n = i / rows;
+        r.m = m0 + i - r.n * rows;
+    }
+    r.kb0 = 0;
+    r.kb1 = j.kb;
+    if (j.splits > 1) {
+        r.kb0 = (int)((int64_t)j.kb * r.split / j.splits);
+        r.kb1 = (int)((int64_t)j.kb * (r.split + 1) / j.splits);
+    }
     return r;
+}
+
+__device__ __forceinline__ bool next_tile(const GemmArgs& g, int worker, int workers, int k, Tile& u)
+{
+    const int t = tile_number(g, worker, workers, k);
+    if (t >= 0)
+        u = tile_at(g, t);
+    return t >= 0;
 }
 
 // ---------------------------------------------------------------------------
 // results: one thread per row of the tile, 32 columns at a time
 // ---------------------------------------------------------------------------
 
-// Maximum and sum of exponentials of 128 columns; the target's column is left
-// out.
-__device__ __forceinline__ void rows_loss(const GemmArgs& g, int col0, int row, float (&z)[kHalf])
+// Maximum and sum of exponentials of `width` columns; the target's column is
+// left out.
+__device__ __forceinline__ void rows_loss(const GemmArgs& g, int part, int col0, int width, int row, float (&z)[kHalf])
 {
     const int64_t target = row < g.n ? target_of(g, row) : -1;
     const int64_t hit64 = target - col0;
-    const bool hits = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < kHalf;
+    const bool hits = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < width;
     const int hit = hits ? (int)hit64 : -1;
-    const int cols = min(kHalf, g.v - col0);
+    const int cols = min(width, g.v - col0);
     if (cols < kHalf) {
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
@@ -218,10 +242,15 @@ __device__ __forceinline__ void rows_loss(const GemmArgs& g, int col0, int row, 
     const float base = top == -INFINITY ? 0.0f : top * kLog2e;
     float s4[4] = {};
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k)
-        s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
-    if (row < g.n && cols > 0)
-        g.part[(int64_t)row * g.part_ld + col0 / kHalf] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+    for (int c = 0; c < kHalf; c += 16) {
+        if (c < cols) {
+#pragma unroll
+            for (int k = c; k < c + 16; ++k)
+                s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
+        }
+    }
+    if (row < g.n)
+        g.part[(int64_t)row * g.part_ld + part] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
 // A result warp's place in its half's box: rows of 128 bytes, the 16-byte
@@ -253,9 +282,9 @@ struct Box {
 
 // dz of 128 columns, rounded to 16 bits once.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int row0, uint32_t tmem, const Box& box)
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, int row0, uint32_t tmem, const Box& box)
 {
-    const int cols = min(kHalf, g.v - g.col0 - col0);  // col0 counts inside the piece
+    const int cols = min(width, g.v - g.col0 - col0);  // col0 counts inside the piece
     const int row = row0 + box.row;
     float base = 0.0f, at_target = 0.0f;
     int hit = -1;
@@ -266,11 +295,11 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int row0, u
         base = fmaf(-g.stats.lse[row], kLog2e, g.exponent);
         at_target = ldexpf(expm1f(-g.stats.loss[row]), (int)g.exponent);
         const int64_t h = target - g.col0 - col0;
-        hit = live && target >= 0 && target < g.v && h >= 0 && h < kHalf ? (int)h : -1;
+        hit = live && target >= 0 && target < g.v && h >= 0 && h < width ? (int)h : -1;
     }
     const bool any_dead = !__all_sync(0xffffffffu, live);
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 64) {
+    for (int c = 0; c < width; c += 64) {
         box.open();
 #pragma unroll
         for (int q = 0; q < 64; q += 32) {
@@ -306,11 +335,11 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int row0, u
 }
 
 // 128 columns of dH's binary32 sums.
-__device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* out, int split, int col0, int row0,
+__device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* out, int split, int col0, int width, int row0,
                                         uint32_t tmem, const Box& box)
 {
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 32) {
+    for (int c = 0; c < width; c += 32) {
         if (col0 + c >= g.d)
             break;
         box.open();
@@ -333,13 +362,13 @@ __device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* ou
 
 // 128 columns of a gradient, final.
 template <bool kBf16>
-__device__ __forceinline__ void rows_final(const GemmArgs& g, const Job& j, const CUtensorMap* out, int col0, int row0,
+__device__ __forceinline__ void rows_final(const GemmArgs& g, const Job& j, const CUtensorMap* out, int col0, int width, int row0,
                                            uint32_t tmem, const Box& box)
 {
     const float scale = g.control->gscale;
     const int row = row0 + box.row;
 #pragma unroll 1
-    for (int c = 0; c < kHalf; c += 64) {
+    for (int c = 0; c < width; c += 64) {
         if (col0 + c >= g.d)
             break;
         if (j.wide)
@@ -418,7 +447,7 @@ __device__ __forceinline__ void by_layout(bool dw, F&& f)
 template <bool kPair, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
 {
-    using S = Shape<kPair>;
+    using S = Shape<kPair, kMode>;
     extern __shared__ uint8_t dyn[];
     __shared__ alignas(8) uint64_t s_full[S::kStages], s_empty[S::kStages], s_acc_full[2], s_acc_empty[2], s_drain;
     __shared__ uint32_t s_tmem;
@@ -468,12 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         uint32_t steps = 0;
         bool ok = true;
         const bool one = elect_one();
-        for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
-            const Tile u = tile_at(g, t);
+        Tile u, then;
+        bool more = next_tile(g, worker, workers, 0, u), after = false;
+        for (int k = 1; ok && more; ++k, more = after, u = then) {
             const CUtensorMap* ma = &g.a[u.job];
             const CUtensorMap* mb = &g.b[u.job];
+            const int share = u.tn / S::kCtas;
             const int row0 = u.m * S::kTileM + (int)rank * kRows;
-            const int col0 = u.n * kTileN + (int)rank * kHalf;
+            const int col0 = u.n * u.tn + (int)rank * share;
+            const uint32_t bytes = (kBytesA + share * (kTileK * 2)) * S::kCtas;
             auto run = [&](auto a_mn, auto b_mn) {
                 for (int kb = u.kb0; kb < u.kb1; ++kb, ++steps, ring.next()) {
                     if (!(ok = mbar_wait_warp(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead)))
@@ -482,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                         uint32_t full = smem_addr(s_full) + ring.at * 8;
                         const uint32_t at_a = tiles_at + ring.at * S::kStageBytes, at_b = at_a + kBytesA;
                         if (rank == 0)
-                            mbar_expect(full, S::kStageBytes * S::kCtas);
+                            mbar_expect(full, bytes);
                         if constexpr (kPair)
                             full = peer_addr(full, 0);
                         auto load = [&](uint32_t at, const CUtensorMap* m, int x, int y) {
@@ -501,13 +533,14 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                         if constexpr (b_mn.value) {
 #pragma unroll
                             for (int q = 0; q < kTileN / S::kCtas / 64; ++q)
-                                load(at_b + q * kBlock, mb, col0 + q * 64, kb * kTileK);
+                                if (q * 64 < share)
+                                    load(at_b + q * kBlock, mb, col0 + q * 64, kb * kTileK);
                         } else {
-#pragma unroll
-                            for (int q = 0; q < 2 / S::kCtas; ++q)
-                                load(at_b + q * (kHalf * kTileK * 2), mb, kb * kTileK, col0 + q * kHalf);
+                            load(at_b, mb, kb * kTileK, col0);
                         }
                     }
+                    if (kb == u.kb0)  // its divisions run under this tile's loads
+                        after = next_tile(g, worker, workers, k, then);
                     __syncwarp();
                 }
             };
@@ -526,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         uint32_t acc = 0;
         bool ok = true;
         const bool one = elect_one();
-        for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
-            const Tile u = tile_at(g, t);
+        Tile u, then;
+        bool more = next_tile(g, worker, workers, 0, u), after = false;
+        for (int k = 1; ok && more; ++k, more = after, u = then) {
             const uint32_t idesc = g.job[u.job].idesc;
             auto run = [&](auto a_mn, auto b_mn) {
                 // one product takes 16 of K: 32 bytes along a row, or 16 rows
@@ -557,14 +591,16 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                         const uint64_t a = desc_a + here * (S::kStageBytes >> 4), b = desc_b + here * (S::kStageBytes >> 4);
                         if (one) {
 #pragma unroll
-                            for (int k = 0; k < kTileK / 16; ++k) {
-                                mma_f16<kPair>(d, a + k * step_a, b + k * step_b, idesc, add);
+                            for (int e = 0; e < kTileK / 16; ++e) {
+                                mma_f16<kPair>(d, a + e * step_a, b + e * step_b, idesc, add);
                                 add = 1;
                             }
                             mma_commit<kPair>(smem_addr(s_empty) + here * 8);
                         }
                         add = 1;
                         __syncwarp();
+                        if (kb == u.kb0)
+                            after = next_tile(g, worker, workers, k, then);
                     }
                     if (ok && one)
                         mma_commit<kPair>(smem_addr(s_acc_full) + buf * 8);
@@ -588,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         box.at = tiles_at + S::kStages * S::kStageBytes + half * kOutBytes;
         box.row_at = box.at + box.row * 128;
         box.first = box.row == 0;
-        const uint32_t lanes_at = tmem + ((uint32_t)(quad * 32) << 16) + half * kHalf;
+        const uint32_t lanes_at = tmem + ((uint32_t)(quad * 32) << 16);
         uint32_t acc = 0;
         bool ok = true;
         auto await = [&]() {
@@ -614,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         for (int k = 0, t; ok && (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
             const Tile u = tile_at(g, t);
             const int row0 = u.m * S::kTileM + (int)rank * kRows;
-            const int col0 = u.n * kTileN + half * kHalf;
+            const int width = u.tn / 2, col0 = u.n * u.tn + half * width;
             if constexpr (kMode == kLoss) {
                 float z[kHalf];
 #pragma unroll
@@ -623,30 +659,32 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 for (int kb = u.kb0; ok && kb < u.kb1; kb += kPromote) {
                     if (!await())
                         break;
-                    const uint32_t at = lanes_at + (acc & 1) * kTileN;
+                    const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
 #pragma unroll
                     for (int c = 0; c < kHalf; c += 16) {
-                        uint32_t r[16];
-                        tmem_load16(at + c, r);
-                        tmem_wait_load(r);
+                        if (c < width) {
+                            uint32_t r[16];
+                            tmem_load16(at + c, r);
+                            tmem_wait_load(r);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            z[c + k] += __uint_as_float(r[k]);
+                            for (int k = 0; k < 16; ++k)
+                                z[c + k] += __uint_as_float(r[k]);
+                        }
                     }
                     give_back();
                 }
                 if (ok)
-                    rows_loss(g, col0, row0 + quad * 32 + lane, z);
+                    rows_loss(g, 2 * u.n + half, col0, width, row0 + quad * 32 + lane, z);
             } else {
                 if (!await())
                     break;
-                const uint32_t at = lanes_at + (acc & 1) * kTileN;
+                const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
                 if constexpr (kMode == kDz)
-                    rows_dz<kBf16>(g, col0, row0, at, box);
+                    rows_dz<kBf16>(g, col0, width, row0, at, box);
                 else if (!g.job[u.job].final)
-                    rows_dh(g, &g.out[u.job], u.split, col0, row0, at, box);
+                    rows_dh(g, &g.out[u.job], u.split, col0, width, row0, at, box);
                 else
-                    rows_final<kBf16>(g, g.job[u.job], &g.out[u.job], col0, row0, at, box);
+                    rows_final<kBf16>(g, g.job[u.job], &g.out[u.job], col0, width, row0, at, box);
                 give_back();
             }
         }
@@ -735,18 +773,19 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
     __shared__ unsigned long long s_valid[kMergeRows];
     __shared__ int s_last, s_bad;
     let_next_start();
-    wait_for_previous();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * kMergeRows + w;
-    float loss = 0.0f;
-    bool valid = false;
-    if (row < g.n) {
+    float loss = 0.0f, zt = 0.0f;
+    bool valid = false, known = false;
+    if (row < g.n) {  // needs the call's inputs only
         const int64_t t = target_of(g, row);
-        const bool known = t >= 0 && t < g.v;
+        known = t >= 0 && t < g.v;
         valid = t != g.ignore;
-        float zt = 0.0f;
         if (valid && known)
             zt = target_logit<kBf16>(a.hidden + (int64_t)row * a.ld_hidden, a.weight + t * a.ld_weight, g.d, lane);
+    }
+    wait_for_previous();
+    if (row < g.n) {
         // maximum and sum of each lane's parts, then of the lanes'
         const float2* p = g.part + (int64_t)row * g.part_ld;
         float top = -INFINITY, sum = 0.0f;
@@ -901,7 +940,9 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 struct Plan {
     bool grad = false, want_dh = false, want_dw = false;
     bool dh_final = false;  // one piece, one sum: no sums in between
-    int64_t parts = 0;      // 128-column parts of the whole vocabulary
+    bool pair = false;      // two CTAs to a tile
+    int64_t tn_loss = 0, tn_dz = 0, tn_grad = 0;  // columns of a tile
+    int64_t parts = 0;      // half tiles of the whole vocabulary
     int64_t piece = 0;      // columns of one piece of the backward pass
     int64_t splits = 1;     // of dH's sums over a piece
     int64_t merges = 0;
@@ -913,12 +954,34 @@ struct Plan {
 constexpr int64_t kPieceBytes = 256ll << 20;
 constexpr int64_t kLeastSplit = 16;  // blocks of 64 in one part of a cut sum
 
+// Columns of a tile: as many as 256, unless narrower tiles, which are a
+// multiple of `quantum`, end the last round sooner.  A tile costs its products
+// (2 clocks a column and block of K) and some 1500 clocks of its own; wider
+// tiles read less, so a narrower one has to gain 3%.  (509 x 50257 x 2048: 240
+// columns, 97 -> 94 us; one row: 176 columns.)
+int64_t tile_columns(int64_t mt, int64_t cols, int64_t kb, int64_t workers, int64_t quantum)
+{
+    int64_t best = 0;
+    double least = 0.0;
+    for (int64_t tn = kTileN; tn >= std::max<int64_t>(32, quantum); tn -= quantum) {
+        const double cost = (double)ceil_div(mt * ceil_div(cols, tn), workers) * (double)(2 * tn * kb + 1500);
+        if (best == 0 || cost < 0.97 * least) {
+            best = tn;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 int make_plan(const mpt_xent_args& a, Plan& p)
 {
     p.want_dh = a.grad_hidden != nullptr;
     p.want_dw = a.grad_weight != nullptr;
     p.grad = p.want_dh || p.want_dw;
-    p.parts = ceil_div(a.v, kHalf);
+    p.pair = a.n > kRows;
+    const int64_t rows = p.pair ? 2 * kRows : kRows, workers = p.pair ? kMaxCtas / 2 : kMaxCtas;
+    p.tn_loss = tile_columns(ceil_div(a.n, rows), a.v, ceil_div(a.d, kTileK), workers, 16);
+    p.parts = 2 * ceil_div(a.v, p.tn_loss);
     p.merges = std::max<int64_t>(1, ceil_div(a.n, kMergeRows));
     size_t at = 0;
     auto region = [&](size_t bytes) {
@@ -935,6 +998,10 @@ int make_plan(const mpt_xent_args& a, Plan& p)
         const int64_t fit = std::max<int64_t>(2048, kPieceBytes / (2 * a.n) / kTileN * kTileN);
         p.piece = std::min(round_up(a.v, kTileN), fit);
         p.off_dz = region((size_t)(a.n * p.piece * 2));
+        p.tn_dz = tile_columns(ceil_div(a.n, rows), p.piece, ceil_div(a.d, kTileK), workers, 128);
+        // few gradient tiles: narrower ones, so that more CTAs have one
+        const int64_t tiles = (p.want_dh ? ceil_div(a.n, rows) : 0) + (p.want_dw ? ceil_div(p.piece, rows) : 0);
+        p.tn_grad = 2 * tiles * ceil_div(a.d, kTileN) <= workers ? 128 : 256;
         if (p.want_dh) {
             // cut dH's sums so that one tile is at most half a CTA's share of the piece's work
             const int64_t kb_v = ceil_div(p.piece, kTileK), kb_n = ceil_div(a.n, kTileK);
@@ -1045,7 +1112,7 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t co
 template <bool kPair, int kMode, bool kBf16>
 cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
 {
-    using S = Shape<kPair>;
+    using S = Shape<kPair, kMode>;
     // once per device; a failure is not remembered
     static std::atomic<uint64_t> set_up{0};
     int dev = -1;
@@ -1103,15 +1170,16 @@ cudaError_t launch_product(bool pair, GemmArgs& g, cudaStream_t st)
 }
 
 void set_job(Job& j, bool pair, bool bf16, int64_t m, int64_t n, int64_t k, int64_t splits, bool a_mn, bool b_mn,
-             int64_t band)
+             int64_t band, int64_t tn)
 {
     const int rows = pair ? 2 * kRows : kRows;
     j.mt = (int32_t)ceil_div(m, rows);
-    j.nt = (int32_t)ceil_div(n, kTileN);
+    j.nt = (int32_t)ceil_div(n, tn);
+    j.tn = (int32_t)tn;
     j.kb = (int32_t)ceil_div(k, kTileK);
     j.splits = (int32_t)std::min<int64_t>(splits, j.kb);
     j.band = (int32_t)std::min<int64_t>(band, j.mt);
-    j.idesc = mma_desc(bf16, a_mn, b_mn, rows, kTileN);
+    j.idesc = mma_desc(bf16, a_mn, b_mn, rows, (int)tn);
     j.tiles = j.mt * j.nt * j.splits;
 }
 
@@ -1121,7 +1189,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     Control* control = reinterpret_cast<Control*>(ws + p.off_ctl);
     float* token = a.token_loss ? a.token_loss : reinterpret_cast<float*>(ws + p.off_token);
     float* lse = a.lse ? a.lse : reinterpret_cast<float*>(ws + p.off_lse);
-    const bool pair = a.n > kRows;
+    const bool pair = p.pair;
     // logits: up to 32 MB of hidden stay in L2 while the vocabulary streams by;
     // gradients: one row of tiles reads its part of dz once, and the whole
     // width of the other operand from L2
@@ -1156,9 +1224,9 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     m.n_valid = a.n_valid;
 
     if (a.n > 0) {
-        set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false, band);
+        set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false, band, p.tn_loss);
         if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows) ||
-            !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, kHalf))
+            !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, (int)p.tn_loss / (pair ? 2 : 1)))
             return MPT_ERR_CUDA;
         if (launch_product<kLoss, kBf16>(pair, g, st) != cudaSuccess)
             return MPT_ERR_CUDA;
@@ -1188,8 +1256,8 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
         const int64_t cols = std::min(p.piece, a.v - c0);
         const uint16_t* wp = w + c0 * a.ld_weight;
         z.col0 = (int32_t)c0;
-        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band);
-        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, kHalf) ||
+        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band, p.tn_dz);
+        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, (int)p.tn_dz / (pair ? 2 : 1)) ||
             !make_map(&z.out[0], kBf16, dz, a.n, cols, p.piece, kRows))
             return MPT_ERR_CUDA;
         if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
@@ -1202,7 +1270,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
         if (p.want_dh) {
             // (a short last piece may add to the first sums only)
             Job& j = q.job[at_h];
-            set_job(j, pair, kBf16, a.n, a.d, cols, splits, false, true, 1);
+            set_job(j, pair, kBf16, a.n, a.d, cols, splits, false, true, 1, p.tn_grad);
             q.add = c0 > 0;
             j.final = p.dh_final;
             j.rows = (int32_t)a.n;
@@ -1217,7 +1285,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
         }
         if (p.want_dw) {
             Job& j = q.job[at_w];
-            set_job(j, pair, kBf16, cols, a.d, a.n, 1, true, true, 1);
+            set_job(j, pair, kBf16, cols, a.d, a.n, 1, true, true, 1, p.tn_grad);
             j.is_dw = j.final = 1;
             j.rows = (int32_t)cols;
             j.wide = wide(a.grad_weight, a.ld_grad_weight);
