@@ -214,14 +214,40 @@ __device__ __forceinline__ bool next_tile(const GemmArgs& g, int worker, int wor
 // results: one thread per row of the tile, 32 columns at a time
 // ---------------------------------------------------------------------------
 
+// What a result thread has to know of its row; read before the accumulator is
+// waited for.
+struct Row {
+    int64_t target;       // -1 beyond the last row
+    float lse, loss;      // kDz
+};
+
+template <int kMode>
+__device__ __forceinline__ Row row_at(const GemmArgs& g, int row)
+{
+    Row r{-1, 0.0f, 0.0f};
+    if (kMode != kGrad && row < g.n) {
+        r.target = target_of(g, row);
+        if (kMode == kDz) {
+            r.lse = g.stats.lse[row];
+            r.loss = g.stats.loss[row];
+        }
+    }
+    return r;
+}
+
+// The target's column among `width` ones from col0 on, or -1.
+__device__ __forceinline__ int hit_at(const GemmArgs& g, int64_t target, int col0, int width)
+{
+    const int64_t h = target - col0;
+    return target >= 0 && target < g.v && target != g.ignore && h >= 0 && h < width ? (int)h : -1;
+}
+
 // Maximum and sum of exponentials of `width` columns; the target's column is
 // left out.
-__device__ __forceinline__ void rows_loss(const GemmArgs& g, int part, int col0, int width, int row, float (&z)[kHalf])
+__device__ __forceinline__ void rows_loss(const GemmArgs& g, int part, int col0, int width, int row, const Row& me,
+                                          float (&z)[kHalf])
 {
-    const int64_t target = row < g.n ? target_of(g, row) : -1;
-    const int64_t hit64 = target - col0;
-    const bool hits = target >= 0 && target < g.v && target != g.ignore && hit64 >= 0 && hit64 < width;
-    const int hit = hits ? (int)hit64 : -1;
+    const int hit = hit_at(g, me.target, col0, width);
     const int cols = min(width, g.v - col0);
     if (cols < kHalf) {
 #pragma unroll
@@ -240,17 +266,21 @@ __device__ __forceinline__ void rows_loss(const GemmArgs& g, int part, int col0,
     const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     // a row of nothing but -inf sums to zero: no inf - inf
     const float base = top == -INFINITY ? 0.0f : top * kLog2e;
-    float s4[4] = {};
+    const uint64_t scale2 = pair_of(kLog2e, kLog2e), base2 = pair_of(-base, -base);
+    uint64_t s4[4] = {};
 #pragma unroll
     for (int c = 0; c < kHalf; c += 16) {
         if (c < cols) {
 #pragma unroll
-            for (int k = c; k < c + 16; ++k)
-                s4[k & 3] += exp2_fast(fmaf(z[k], kLog2e, -base));
+            for (int k = c; k < c + 16; k += 2) {
+                const float2 e = of_pair(fma2(pair_of(z[k], z[k + 1]), scale2, base2));
+                s4[(k / 2) & 3] = add2(s4[(k / 2) & 3], pair_of(exp2_fast(e.x), exp2_fast(e.y)));
+            }
         }
     }
+    const float2 sum = of_pair(add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])));
     if (row < g.n)
-        g.part[(int64_t)row * g.part_ld + part] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        g.part[(int64_t)row * g.part_ld + part] = make_float2(top, sum.x + sum.y);
 }
 
 // A result warp's place in its half's box: rows of 128 bytes, the 16-byte
@@ -282,49 +312,53 @@ struct Box {
 
 // dz of 128 columns, rounded to 16 bits once.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, int row0, uint32_t tmem, const Box& box)
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, int row0, const Row& me, uint32_t tmem,
+                                        const Box& box)
 {
     const int cols = min(width, g.v - g.col0 - col0);  // col0 counts inside the piece
-    const int row = row0 + box.row;
-    float base = 0.0f, at_target = 0.0f;
-    int hit = -1;
-    bool live = false;
-    if (row < g.n) {
-        const int64_t target = target_of(g, row);
-        live = target != g.ignore;
-        base = fmaf(-g.stats.lse[row], kLog2e, g.exponent);
-        at_target = ldexpf(expm1f(-g.stats.loss[row]), (int)g.exponent);
-        const int64_t h = target - g.col0 - col0;
-        hit = live && target >= 0 && target < g.v && h >= 0 && h < width ? (int)h : -1;
-    }
-    const bool any_dead = !__all_sync(0xffffffffu, live);
+    const int hit = hit_at(g, me.target, g.col0 + col0, width);
+    const bool live = row0 + box.row < g.n && me.target != g.ignore;
+    const bool edge = cols < width || !__all_sync(0xffffffffu, live);
+    const float base = fmaf(-me.lse, kLog2e, g.exponent);
+    const uint64_t scale2 = pair_of(kLog2e, kLog2e), base2 = pair_of(base, base);
 #pragma unroll 1
     for (int c = 0; c < width; c += 64) {
+        __syncwarp();
+        uint32_t r[2][32];
+        tmem_load32(tmem + c, r[0]);
+        tmem_load32(tmem + c + 32, r[1]);
+        tmem_wait_load(r[0]);
+        tmem_wait_load(r[1]);
+        const bool hits = __any_sync(0xffffffffu, hit >= c && hit < c + 64);
+        uint32_t o[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            float* z = reinterpret_cast<float*>(r[q]);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                const float2 e = of_pair(fma2(pair_of(z[k], z[k + 1]), scale2, base2));
+                z[k] = exp2_fast(e.x);
+                z[k + 1] = exp2_fast(e.y);
+            }
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    z[k] = live && c + 32 * q + k < cols ? z[k] : 0.0f;
+            }
+            if (hits) {
+                const float at_target = ldexpf(expm1f(-me.loss), (int)g.exponent);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    z[k] = c + 32 * q + k == hit ? at_target : z[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                o[16 * q + k] = pack2<kBf16>(z[2 * k], z[2 * k + 1]);
+        }
         box.open();
 #pragma unroll
-        for (int q = 0; q < 64; q += 32) {
-            uint32_t r[32];
-            tmem_load32(tmem + c + q, r);
-            tmem_wait_load(r);
-            float* z = reinterpret_cast<float*>(r);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                z[k] = exp2_fast(fmaf(z[k], kLog2e, base));
-            if (c + q + 32 > cols || any_dead) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    z[k] = live && c + q + k < cols ? z[k] : 0.0f;
-            }
-            if (__any_sync(0xffffffffu, hit >= c + q && hit < c + q + 32)) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    z[k] = c + q + k == hit ? at_target : z[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                box.put(q / 8 + k, pack2<kBf16>(z[8 * k], z[8 * k + 1]), pack2<kBf16>(z[8 * k + 2], z[8 * k + 3]),
-                        pack2<kBf16>(z[8 * k + 4], z[8 * k + 5]), pack2<kBf16>(z[8 * k + 6], z[8 * k + 7]));
-        }
+        for (int k = 0; k < 8; ++k)
+            box.put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         box.close();
         if (box.first) {
             if (c < cols && row0 < g.n)
@@ -342,10 +376,11 @@ __device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* ou
     for (int c = 0; c < width; c += 32) {
         if (col0 + c >= g.d)
             break;
-        box.open();
+        __syncwarp();
         uint32_t r[32];
         tmem_load32(tmem + c, r);
         tmem_wait_load(r);
+        box.open();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             box.put(k, r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
@@ -371,33 +406,31 @@ __device__ __forceinline__ void rows_final(const GemmArgs& g, const Job& j, cons
     for (int c = 0; c < width; c += 64) {
         if (col0 + c >= g.d)
             break;
-        if (j.wide)
+        __syncwarp();
+        uint32_t r[2][32], o[32];
+        tmem_load32(tmem + c, r[0]);
+        tmem_load32(tmem + c + 32, r[1]);
+        tmem_wait_load(r[0]);
+        tmem_wait_load(r[1]);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float* z = reinterpret_cast<const float*>(r[e / 16]) + 2 * (e % 16);
+            o[e] = pack2<kBf16>(z[0] * scale, z[1] * scale);
+        }
+        if (j.wide) {
             box.open();
 #pragma unroll
-        for (int q = 0; q < 64; q += 32) {
-            uint32_t r[32];
-            tmem_load32(tmem + c + q, r);
-            tmem_wait_load(r);
-            const float* z = reinterpret_cast<const float*>(r);
-            uint32_t o[16];
+            for (int k = 0; k < 8; ++k)
+                box.put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else if (row < j.rows) {
+            uint16_t* to = j.to + (int64_t)row * j.ld + col0 + c;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                o[e] = pack2<kBf16>(z[2 * e] * scale, z[2 * e + 1] * scale);
-            if (j.wide) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    box.put(q / 8 + k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            } else if (row < j.rows) {
-                uint16_t* to = j.to + (int64_t)row * j.ld + col0 + c + q;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (col0 + c + q + 2 * e < g.d) {
-                        to[2 * e] = (uint16_t)(o[e] & 0xFFFFu);
-                        to[2 * e + 1] = (uint16_t)(o[e] >> 16);
-                    }
+            for (int e = 0; e < 32; ++e) {
+                if (col0 + c + 2 * e < g.d) {
+                    to[2 * e] = (uint16_t)(o[e] & 0xFFFFu);
+                    to[2 * e + 1] = (uint16_t)(o[e] >> 16);
                 }
             }
-            __syncwarp();
         }
         if (j.wide) {
             box.close();
@@ -651,36 +684,46 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             const Tile u = tile_at(g, t);
             const int row0 = u.m * S::kTileM + (int)rank * kRows;
             const int width = u.tn / 2, col0 = u.n * u.tn + half * width;
+            const Row me = row_at<kMode>(g, row0 + quad * 32 + lane);
             if constexpr (kMode == kLoss) {
                 float z[kHalf];
-#pragma unroll
-                for (int k = 0; k < kHalf; ++k)
-                    z[k] = 0.0f;
                 for (int kb = u.kb0; ok && kb < u.kb1; kb += kPromote) {
                     if (!await())
                         break;
                     const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
+                    if (kb == u.kb0) {
+                        // the first part goes straight to its place; whole
+                        // 32 columns are read (what lies beyond is masked)
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 16) {
-                        if (c < width) {
-                            uint32_t r[16];
-                            tmem_load16(at + c, r);
-                            tmem_wait_load(r);
+                        for (int c = 0; c < kHalf; c += 32)
+                            if (c < width)
+                                tmem_load32(at + c, *reinterpret_cast<uint32_t(*)[32]>(z + c));
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                z[c + k] += __uint_as_float(r[k]);
+                        for (int c = 0; c < kHalf; c += 32)
+                            tmem_wait_load(*reinterpret_cast<uint32_t(*)[32]>(z + c));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 16) {
+                            if (c < width) {
+                                uint32_t r[16];
+                                tmem_load16(at + c, r);
+                                tmem_wait_load(r);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    z[c + k] += __uint_as_float(r[k]);
+                            }
                         }
                     }
                     give_back();
                 }
                 if (ok)
-                    rows_loss(g, 2 * u.n + half, col0, width, row0 + quad * 32 + lane, z);
+                    rows_loss(g, 2 * u.n + half, col0, width, row0 + quad * 32 + lane, me, z);
             } else {
                 if (!await())
                     break;
                 const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
                 if constexpr (kMode == kDz)
-                    rows_dz<kBf16>(g, col0, width, row0, at, box);
+                    rows_dz<kBf16>(g, col0, width, row0, me, at, box);
                 else if (!g.job[u.job].final)
                     rows_dh(g, &g.out[u.job], u.split, col0, width, row0, at, box);
                 else
