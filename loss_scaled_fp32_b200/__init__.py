@@ -517,67 +517,58 @@ XentLoss = collections.namedtuple("XentLoss", "loss token_loss lse n_valid")
 XentGrad = collections.namedtuple("XentGrad", "loss token_loss lse n_valid grad_hidden grad_weight")
 
 
-def _rows(t, what, like=None):
-    """The row distance of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{what} must be a 2-D CUDA tensor")
-    n, d = t.shape
-    ld, step = t.stride()
+def _rows(t, what, dtype, device, shape=None):
+    """The row distance of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype != dtype or t.device != device or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must be a 2-D tensor of the type, device and width of hidden"
+                         + (f" and the shape {tuple(shape)}" if shape is not None else ""))
+    (n, d), (ld, step) = t.shape, t.stride()
     if step != 1 and d > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{what} must have the type and device of hidden")
     return ld if n > 1 else max(ld, (d + 7) // 8 * 8)
 
 
 def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, grad_weight, stream):
     import torch
     L = lib()
-    a = XentArgs()
-    L.mpt_xent_args_init(ctypes.byref(a))
-    a.ld_hidden, a.ld_weight = _rows(hidden, "hidden"), _rows(weight, "weight", hidden)
-    a.type = _type_code(hidden.dtype)
-    n, d = a.n, a.d = hidden.shape
-    a.v = weight.shape[0]
-    dev = hidden.device
-    if weight.shape[1] != d:
+    dev, dtype = hidden.device, hidden.dtype
+    if dev.type != "cuda":
+        raise ValueError("hidden must be a CUDA tensor")
+    ld_h = _rows(hidden, "hidden", dtype, dev)
+    n, d = hidden.shape
+    ld_w = _rows(weight, "weight", dtype, dev)
+    v, width = weight.shape
+    if width != d:
         raise ValueError("hidden and weight must have rows of one width")
     if targets.shape != (n,) or targets.device != dev or not targets.is_contiguous() or \
-            targets.dtype not in (torch.int32, torch.int64):
+            targets.dtype not in (torch.int64, torch.int32):
         raise ValueError("targets must be one int32 or int64 per row of hidden, contiguous, on its device")
     if reduction not in ("mean", "sum"):
         raise ValueError("reduction is 'mean' or 'sum'")
-    a.target_bytes = targets.element_size()
-    a.ignore_index = ignore_index
-    a.reduction = MPT_XENT_SUM if reduction == "sum" else MPT_XENT_MEAN
-    a.scale, a.d_scale = _scale_args(scale, dev)
-    a.hidden, a.weight, a.targets = hidden.data_ptr(), weight.data_ptr(), targets.data_ptr()
+    host_scale, dev_scale = _scale_args(scale, dev)
     # what the call allocates belongs to the stream that it runs on
     with _on(dev, stream):
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
-        n_valid = torch.empty(1, dtype=torch.int64, device=dev)
-        token_loss = torch.empty(n, dtype=torch.float32, device=dev)
-        lse = torch.empty(n, dtype=torch.float32, device=dev)
+        f32 = torch.float32
+        loss, n_valid = hidden.new_empty(1, dtype=f32), targets.new_empty(1, dtype=torch.int64)
+        token_loss, lse = hidden.new_empty(n, dtype=f32), hidden.new_empty(n, dtype=f32)
+        gh = gw = None
+        ld_gh = ld_gw = 0
         if grad_hidden is not None and grad_hidden is not False:
-            if grad_hidden is True:
-                grad_hidden = torch.empty((n, d), dtype=hidden.dtype, device=dev)
-            elif grad_hidden.shape != hidden.shape:
-                raise ValueError(f"grad_hidden must have the shape {tuple(hidden.shape)}")
-            a.ld_grad_hidden, a.grad_hidden = _rows(grad_hidden, "grad_hidden", hidden), grad_hidden.data_ptr()
+            gh = hidden.new_empty((n, d)) if grad_hidden is True else grad_hidden
+            ld_gh = _rows(gh, "grad_hidden", dtype, dev, hidden.shape)
         if grad_weight is not None and grad_weight is not False:
-            if grad_weight is True:
-                grad_weight = torch.empty((a.v, d), dtype=hidden.dtype, device=dev)
-            elif grad_weight.shape != weight.shape:
-                raise ValueError(f"grad_weight must have the shape {tuple(weight.shape)}")
-            a.ld_grad_weight, a.grad_weight = _rows(grad_weight, "grad_weight", hidden), grad_weight.data_ptr()
-        a.loss, a.n_valid = loss.data_ptr(), n_valid.data_ptr()
-        a.token_loss, a.lse = token_loss.data_ptr(), lse.data_ptr()
+            gw = hidden.new_empty((v, d)) if grad_weight is True else grad_weight
+            ld_gw = _rows(gw, "grad_weight", dtype, dev, weight.shape)
+        a = XentArgs(_type_code(dtype), targets.element_size(), n, v, d, hidden.data_ptr(), ld_h,
+                     weight.data_ptr(), ld_w, targets.data_ptr(), ignore_index,
+                     MPT_XENT_SUM if reduction == "sum" else MPT_XENT_MEAN, host_scale, dev_scale,
+                     loss.data_ptr(), token_loss.data_ptr(), lse.data_ptr(), n_valid.data_ptr(),
+                     None if gh is None else gh.data_ptr(), ld_gh, None if gw is None else gw.data_ptr(), ld_gw)
         nbytes = ctypes.c_size_t()
         _check(L.mpt_xent_workspace_bytes(ctypes.byref(a), ctypes.byref(nbytes)), "mpt_xent_workspace_bytes")
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+        ws = hidden.new_empty(nbytes.value, dtype=torch.uint8)
         _check(L.mpt_xent(ctypes.byref(a), ws.data_ptr(), nbytes.value, _stream_ptr(stream, dev)), "mpt_xent")
-    return loss, token_loss, lse, n_valid, None if grad_hidden is False else grad_hidden, \
-        None if grad_weight is False else grad_weight
+    return loss, token_loss, lse, n_valid, gh, gw
 
 
 def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stream=None):

@@ -751,6 +751,164 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------------------
+// the forward pass of a few rows
+// ---------------------------------------------------------------------------
+
+// One to four rows of hidden: the head is read once and that bounds the pass,
+// so every warp streams whole rows of it (four at a time, eight 16-byte loads
+// in flight per lane) past the rows of hidden, which stand in shared memory as
+// binary32.  The tensor cores' 128-byte pieces of 2 KB rows reach half of the
+// memory rate.
+constexpr int kFew = 4;
+constexpr int kFewThreads = 256;
+constexpr int few_ctas(int64_t rows) { return rows > 2 ? 2 : 3; }  // per SM
+constexpr int kFewSmem = 160 * 1024;
+
+// Sums of four values over a warp: lane l gets that of row (l >> 3) & 3.
+__device__ __forceinline__ float sum_rows(float a0, float a1, float a2, float a3, int lane)
+{
+    const bool up = lane & 16, left = lane & 8;
+    const float c0 = (up ? a2 : a0) + __shfl_xor_sync(0xffffffffu, up ? a0 : a2, 16);
+    const float c1 = (up ? a3 : a1) + __shfl_xor_sync(0xffffffffu, up ? a1 : a3, 16);
+    float d = (left ? c1 : c0) + __shfl_xor_sync(0xffffffffu, left ? c0 : c1, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        d += __shfl_xor_sync(0xffffffffu, d, o);
+    return d;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (kBf16) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            x[2 * e] = f.x;
+            x[2 * e + 1] = f.y;
+        }
+    }
+}
+
+// Adds (m2, s2), a maximum and a sum of exponentials, to (m, s).
+__device__ __forceinline__ void add_part(float& m, float& s, float m2, float s2)
+{
+    const float top = fmaxf(m, m2), base = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_fast((m - base) * kLog2e) + s2 * exp2_fast((m2 - base) * kLog2e);
+    m = top;
+}
+
+template <bool kBf16, int kN>
+__global__ void __launch_bounds__(kFewThreads, few_ctas(kN))
+xent_few_kernel(const __grid_constant__ GemmArgs g, const uint16_t* hidden, int64_t ld_hidden, const uint16_t* weight,
+                int64_t ld_weight)
+{
+    extern __shared__ float4 s_hidden[];  // [kN][steps][2][32]
+    __shared__ float2 s_part[kFewThreads / 32][kN];
+    let_next_start();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int steps = (g.d + 255) / 256;
+    for (int i = threadIdx.x; i < kN * steps * 32; i += kFewThreads) {
+        const int n = i / (steps * 32), k = (i - n * steps * 32) * 8;
+        float x[8] = {};
+        if (n < g.n && k < g.d)
+            widen8<kBf16>(*reinterpret_cast<const uint4*>(hidden + n * ld_hidden + k), x);
+        float4* to = s_hidden + (n * steps + k / 256) * 64 + (k & 255) / 8;
+        to[0] = make_float4(x[0], x[1], x[2], x[3]);
+        to[32] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        g.control->ticket = 0;
+    int64_t target[kN];
+    float m[kN], s[kN];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        target[n] = n < g.n ? target_of(g, n) : -1;
+        if (target[n] == g.ignore)
+            target[n] = -1;
+        m[n] = -INFINITY;
+        s[n] = 0.0f;
+    }
+    __syncthreads();
+
+    const int warps = gridDim.x * (kFewThreads / 32);
+    for (int64_t r0 = (int64_t)(blockIdx.x * (kFewThreads / 32) + w) * 4; r0 < g.v; r0 += (int64_t)warps * 4) {
+        const uint16_t* row[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            row[q] = weight + min(r0 + q, (int64_t)g.v - 1) * ld_weight + lane * 8;
+        float acc[4][kN] = {};
+        auto step = [&](const uint4 (&v)[4], int i) {
+            float x[4][8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                widen8<kBf16>(v[q], x[q]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                const float4 lo = s_hidden[(n * steps + i) * 64 + lane], hi = s_hidden[(n * steps + i) * 64 + 32 + lane];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    acc[q][n] = fmaf(x[q][0], lo.x, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][1], lo.y, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][2], lo.z, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][3], lo.w, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][4], hi.x, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][5], hi.y, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][6], hi.z, acc[q][n]);
+                    acc[q][n] = fmaf(x[q][7], hi.w, acc[q][n]);
+                }
+            }
+        };
+        int i = 0;
+        for (; (i + 2) * 256 <= g.d; i += 2) {
+            uint4 a[4], b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                a[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + i * 256));
+                b[q] = __ldcs(reinterpret_cast<const uint4*>(row[q] + (i + 1) * 256));
+            }
+            step(a, i);
+            step(b, i + 1);
+        }
+        for (; i * 256 < g.d; ++i) {
+            uint4 a[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                a[q] = i * 256 + lane * 8 < g.d ? __ldcs(reinterpret_cast<const uint4*>(row[q] + i * 256))
+                                                : make_uint4(0, 0, 0, 0);
+            step(a, i);
+        }
+        const int64_t u = r0 + ((lane >> 3) & 3);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const float z = sum_rows(acc[0][n], acc[1][n], acc[2][n], acc[3][n], lane);
+            if (u < g.v && u != target[n])
+                add_part(m[n], s[n], z, 1.0f);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int o = 8; o <= 16; o <<= 1)
+            add_part(m[n], s[n], __shfl_xor_sync(0xffffffffu, m[n], o), __shfl_xor_sync(0xffffffffu, s[n], o));
+        if (lane == 0)
+            s_part[w][n] = make_float2(m[n], s[n]);
+    }
+    __syncthreads();
+    if (threadIdx.x < kN && threadIdx.x < g.n) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFewThreads / 32; ++k)
+            add_part(top, sum, s_part[k][threadIdx.x].x, s_part[k][threadIdx.x].y);
+        g.part[(int64_t)threadIdx.x * g.part_ld + blockIdx.x] = make_float2(top, sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // row losses, the mean, and dH
 // ---------------------------------------------------------------------------
 
@@ -769,19 +927,13 @@ __device__ __forceinline__ float target_logit(const uint16_t* h, const uint16_t*
     float s0 = 0.0f, s1 = 0.0f;
     for (int k = lane * 8; k < d; k += 256) {
         const uint4 a = __ldg(reinterpret_cast<const uint4*>(h + k)), b = __ldg(reinterpret_cast<const uint4*>(w + k));
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+        float x[8], y[8];
+        widen8<kBf16>(a, x);
+        widen8<kBf16>(b, y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float2 p, q;
-            if constexpr (kBf16) {
-                p = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u));
-                q = make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u));
-            } else {
-                p = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
-                q = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-            }
-            s0 = fmaf(p.x, q.x, s0);
-            s1 = fmaf(p.y, q.y, s1);
+        for (int e = 0; e < 8; e += 2) {
+            s0 = fmaf(x[e], y[e], s0);
+            s1 = fmaf(x[e + 1], y[e + 1], s1);
         }
     }
     float s = s0 + s1;
@@ -984,6 +1136,8 @@ struct Plan {
     bool grad = false, want_dh = false, want_dw = false;
     bool dh_final = false;  // one piece, one sum: no sums in between
     bool pair = false;      // two CTAs to a tile
+    bool few = false;       // the forward pass of up to kFew rows
+    int64_t few_rows = 0, few_smem = 0;
     int64_t tn_loss = 0, tn_dz = 0, tn_grad = 0;  // columns of a tile
     int64_t parts = 0;      // half tiles of the whole vocabulary
     int64_t piece = 0;      // columns of one piece of the backward pass
@@ -1025,6 +1179,13 @@ int make_plan(const mpt_xent_args& a, Plan& p)
     const int64_t rows = p.pair ? 2 * kRows : kRows, workers = p.pair ? kMaxCtas / 2 : kMaxCtas;
     p.tn_loss = tile_columns(ceil_div(a.n, rows), a.v, ceil_div(a.d, kTileK), workers, 16);
     p.parts = 2 * ceil_div(a.v, p.tn_loss);
+    p.few_rows = a.n <= 1 ? 1 : a.n <= 2 ? 2 : kFew;
+    p.few_smem = p.few_rows * round_up(a.d, 256) * 4;
+    if (a.n <= kFew && p.few_smem <= kFewSmem) {
+        p.few = true;
+        p.parts = std::min<int64_t>(ceil_div(a.v, 4 * kFewThreads / 32),
+                                    kMaxCtas * std::min<int64_t>(few_ctas(p.few_rows), 220 * 1024 / p.few_smem));
+    }
     p.merges = std::max<int64_t>(1, ceil_div(a.n, kMergeRows));
     size_t at = 0;
     auto region = [&](size_t bytes) {
@@ -1152,23 +1313,48 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t co
                     box_rows);
 }
 
-template <bool kPair, int kMode, bool kBf16>
-cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
+// Lets a kernel use `bytes` of shared memory, once per device; a failure is
+// not remembered.
+template <class K>
+cudaError_t allow_smem(std::atomic<uint64_t>& set_up, K kernel, int bytes)
 {
-    using S = Shape<kPair, kMode>;
-    // once per device; a failure is not remembered
-    static std::atomic<uint64_t> set_up{0};
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (!(set_up.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(xent_product_kernel<kPair, kMode, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess)
-            return e;
+    if (set_up.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
         set_up.fetch_or(bit, std::memory_order_release);
-    }
+    return e;
+}
+
+template <bool kBf16, int kN>
+cudaError_t launch_few(const GemmArgs& g, const mpt_xent_args& a, const Plan& p, cudaStream_t st)
+{
+    static std::atomic<uint64_t> set_up{0};
+    const cudaError_t e = allow_smem(set_up, xent_few_kernel<kBf16, kN>, kFewSmem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)p.parts);
+    lc.blockDim = dim3(kFewThreads);
+    lc.dynamicSmemBytes = (size_t)p.few_smem;
+    lc.stream = st;
+    return cudaLaunchKernelEx(&lc, xent_few_kernel<kBf16, kN>, g, static_cast<const uint16_t*>(a.hidden), a.ld_hidden,
+                              static_cast<const uint16_t*>(a.weight), a.ld_weight);
+}
+
+template <bool kPair, int kMode, bool kBf16>
+cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
+{
+    using S = Shape<kPair, kMode>;
+    static std::atomic<uint64_t> set_up{0};
+    const cudaError_t e = allow_smem(set_up, xent_product_kernel<kPair, kMode, kBf16>, S::kSmem);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t lc = {};
     const int32_t tiles = g.job[0].tiles + g.job[1].tiles;
     const int32_t workers = std::min(tiles, kMaxCtas / S::kCtas);
@@ -1266,7 +1452,13 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     m.loss = a.loss;
     m.n_valid = a.n_valid;
 
-    if (a.n > 0) {
+    if (p.few && a.n > 0) {
+        const cudaError_t e = p.few_rows == 1   ? launch_few<kBf16, 1>(g, a, p, st)
+                              : p.few_rows == 2 ? launch_few<kBf16, 2>(g, a, p, st)
+                                                : launch_few<kBf16, kFew>(g, a, p, st);
+        if (e != cudaSuccess)
+            return MPT_ERR_CUDA;
+    } else if (a.n > 0) {
         set_job(g.job[0], pair, kBf16, a.n, a.v, a.d, 1, false, false, band, p.tn_loss);
         if (!make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows) ||
             !make_map(&g.b[0], kBf16, a.weight, a.v, a.d, a.ld_weight, (int)p.tn_loss / (pair ? 2 : 1)))
@@ -1291,6 +1483,8 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     uint16_t* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
     auto wide = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
     float* dh = reinterpret_cast<float*>(ws + p.off_dh);
+    if (p.few && !make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows))
+        return MPT_ERR_CUDA;
     GemmArgs z = g;
     GemmArgs q = g;
     const uint16_t* w = static_cast<const uint16_t*>(a.weight);
