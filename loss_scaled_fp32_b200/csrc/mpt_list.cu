@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int kGranule = 512;      // bytes: one 16-byte load per lane
 constexpr int kPtrSlots = 4;       // pointer tables held on the device at once
 constexpr int kLongRuns = 128;
@@ -166,14 +166,20 @@ __device__ __forceinline__ double run_square(const void* base, int64_t begin, in
             }
         }
     }
-    for (; i < nv; i += 32) {
-        const uint4 q = __ldg(v + i);
-        float x[kPer];
-        widen<kType>(q, x);
+    if (i - lane < nv) {  // the last, partly filled batch in one round, too
+        uint4 q[kU];
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-            a0 = fma((double)x[e], (double)x[e], a0);
-            a1 = fma((double)x[e + 1], (double)x[e + 1], a1);
+        for (int k = 0; k < kU; ++k)
+            q[k] = i + k * 32 < nv ? __ldg(v + i + k * 32) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            float x[kPer];
+            widen<kType>(q[k], x);
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) {
+                a0 = fma((double)x[e], (double)x[e], a0);
+                a1 = fma((double)x[e + 1], (double)x[e + 1], a1);
+            }
         }
     }
     if (lane < head) {
@@ -386,9 +392,10 @@ __device__ __forceinline__ typename Elem<kOut>::T scaled(float x, float inv, flo
     return Elem<kOut>::down(__fmul_rn(x, coef));
 }
 
-// One batch of kN 16-byte input vectors, 32 lanes apart, scaled and stored.
-template <int kIn, int kOut, int kN>
-__device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::T* o, int64_t i,
+// One batch of kN 16-byte input vectors, 32 lanes apart, scaled and stored;
+// kEnds: those from `end` on are left out.
+template <int kIn, int kOut, int kN, bool kEnds>
+__device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::T* o, int64_t i, int64_t end,
                                            bool wide, float inv, float coef, bool unscale)
 {
     using TO = typename Elem<kOut>::T;
@@ -396,9 +403,10 @@ __device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::
     uint4 q[kN];
 #pragma unroll
     for (int k = 0; k < kN; ++k)
-        q[k] = v[i + k * 32];
+        q[k] = !kEnds || i + k * 32 < end ? v[i + k * 32] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
+        const bool in = !kEnds || i + k * 32 < end;
         float x[kPer];
         widen<kIn>(q[k], x);
         TO y[kPer];
@@ -406,7 +414,7 @@ __device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::
         for (int e = 0; e < kPer; ++e)
             y[e] = scaled<kIn, kOut>(x[e], inv, coef, unscale);
         TO* to = o + (i + k * 32) * kPer;
-        if (wide) {
+        if (in && wide) {
             // kPer outputs are 8, 16 or 32 bytes
             constexpr int kBytes = kPer * (int)sizeof(TO);
             uint32_t w[kBytes / 4];
@@ -426,7 +434,7 @@ __device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::
                 for (int e = 0; e < kBytes / 16; ++e)
                     reinterpret_cast<uint4*>(to)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
-        } else {
+        } else if (in) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e)
                 to[e] = y[e];
@@ -457,10 +465,9 @@ __device__ __forceinline__ void run_scale(const void* base, void* out, int64_t b
     if (tail + lane < len)
         o[tail + lane] = scaled<kIn, kOut>(Elem<kIn>::up(g[tail + lane]), inv, coef, unscale);
     const int64_t full = nv / (kU * 32);
-    for (int64_t i = full * (kU * 32) + lane; i < nv; i += 32)
-        scale_vecs<kIn, kOut, 1>(v, ov, i, wide, inv, coef, unscale);
+    scale_vecs<kIn, kOut, kU, true>(v, ov, full * (kU * 32) + lane, nv, wide, inv, coef, unscale);
     for (int64_t b = full - 1; b >= 0; --b)
-        scale_vecs<kIn, kOut, kU>(v, ov, b * (kU * 32) + lane, wide, inv, coef, unscale);
+        scale_vecs<kIn, kOut, kU, false>(v, ov, b * (kU * 32) + lane, nv, wide, inv, coef, unscale);
     if (lane < head)
         o[lane] = scaled<kIn, kOut>(Elem<kIn>::up(g[lane]), inv, coef, unscale);
 }
@@ -484,26 +491,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) list_clip_kernel(ListArg
     const int lane = threadIdx.x & 31;
     const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int first = a.warp_runs[warp], last = a.warp_runs[warp + 1];  // written at creation
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Totals t = totals(a, s_sum, &s_tot);
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        write_result(a, t);
-    if (a.want_tensor_norms)
-        write_tensor_norms(a);
-    const bool unscale = a.unscale != 0 && t.inv_scale != 1.0f;
-    if (a.identity_skips && !unscale && t.coef == 1.0f)
-        return;  // in place, one factor of exactly 1
-    const int blocks = (last - first + 31) / 32;
-    for (int b = blocks - 1; b >= 0; --b) {
-        const int r0 = first + b * 32;
-        Run mine{};
-        const void* base = nullptr;
-        void* to = nullptr;
+    // the last 32 runs and their addresses are at hand when the wait ends
+    int r0 = first + (last - first - 1) / 32 * 32;
+    Run mine{};
+    const void* base = nullptr;
+    void* to = nullptr;
+    auto fetch = [&]() {
         if (r0 + lane < last) {
             mine = a.runs[r0 + lane];
             base = a.grads[mine.tensor];
             to = a.outs[mine.tensor];
         }
+    };
+    if (first < last)
+        fetch();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Totals t = totals(a, s_sum, &s_tot);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        write_result(a, t);
+    const bool unscale = a.unscale != 0 && t.inv_scale != 1.0f;
+    const bool skip = a.identity_skips && !unscale && t.coef == 1.0f;  // in place, one factor of exactly 1
+    while (!skip && first < last) {
         for (int k = min(32, last - r0) - 1; k >= 0; --k) {
             const int64_t begin = __shfl_sync(0xffffffffu, mine.begin, k);
             const int64_t len = __shfl_sync(0xffffffffu, mine.len, k);
@@ -520,7 +528,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) list_clip_kernel(ListArg
             else
                 run_scale_to<MPT_F32>(otype, g, o, begin, len, lane, t.inv_scale, t.coef, unscale);
         }
+        if (r0 == first)
+            break;
+        r0 -= 32;
+        fetch();
     }
+    if (a.want_tensor_norms)
+        write_tensor_norms(a);
 }
 
 // ---------------------------------------------------------------------------
@@ -557,7 +571,9 @@ int build_plan(const int64_t* sizes, const int32_t* types, const int32_t* out_ty
             return MPT_ERR_INVALID_ARG;
     }
     const int64_t warps_max = (int64_t)kMaxCtas * kWarps;
-    const int64_t warps_wanted = std::max<int64_t>(1, std::min(units, warps_max));
+    // at least 2 KB (four loads a lane) to a warp: a million FP16 values are done
+    // by 128 CTAs in 8.2 us, by 512 CTAs of a quarter of the work in 10.4 us
+    const int64_t warps_wanted = std::max<int64_t>(1, std::min((units + 3) / 4, warps_max));
     p.ctas = (int32_t)((warps_wanted + kWarps - 1) / kWarps);
     const int64_t warps = (int64_t)p.ctas * kWarps;
     p.warp_runs.assign(1, 0);
