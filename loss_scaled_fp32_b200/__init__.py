@@ -319,6 +319,22 @@ class MPT:
         import torch
         return self.workspace[off:off + 4].view(torch.float32)
 
+    def head_grad(self, i, hidden, targets, grad_weight=True, ignore_index=-100, reduction="mean",
+                  grad_hidden=True, stream=None):
+        """Loss and gradients of a linear head whose weight is tensor ``i``
+        (classes x width, row-major): :func:`xent_grad` with the FP16 working
+        copy and the device loss scale, as a step's first half.
+
+            r = opt.head_grad(0, hidden, targets, grad_weight=grads[0].view(v, d))
+            ...                       # r.grad_hidden goes back through the model
+            opt.step_async(grads, lr, momentum, weight_decay)
+        """
+        if hidden.dim() != 2 or hidden.shape[1] == 0 or self.sizes[i] % hidden.shape[1]:
+            raise ValueError(f"tensor {i} has no rows of the width of hidden")
+        weight = self.w16(i).view(-1, hidden.shape[1])
+        return xent_grad(hidden, weight, targets, scale=self.device_scale(), ignore_index=ignore_index,
+                         reduction=reduction, grad_hidden=grad_hidden, grad_weight=grad_weight, stream=stream)
+
     def step_partial(self, grads, stream=None):
         """Sharded step, phase 2: queue the check pass; returns a 32-byte
         uint8 CUDA tensor aliasing this rank's record."""
@@ -532,8 +548,8 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
     import torch
     L = lib()
     dev, dtype = hidden.device, hidden.dtype
-    if dev.type != "cuda":
-        raise ValueError("hidden must be a CUDA tensor")
+    if dev.type != "cuda" or dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("hidden must be a float16 or bfloat16 CUDA tensor")
     ld_h = _rows(hidden, "hidden", dtype, dev)
     n, d = hidden.shape
     ld_w = _rows(weight, "weight", dtype, dev)

@@ -117,9 +117,9 @@ def _reference(h, w, t, scale, mean=True):
     n, d = H.shape
     v = W.shape[0]
     z = H @ W.t()
-    a = (H.abs() @ W.abs().t()).max() if n else torch.tensor(0.0)
+    a = float((H.abs() @ W.abs().t()).max()) if n else 0.0
     live = t != IGNORE
-    at = torch.where(live, t, 0)
+    at = torch.where(live, t, 0).long()
     lse = torch.logsumexp(z, 1)
     loss = torch.where(live, lse - z.gather(1, at[:, None])[:, 0], 0.0)
     k = int(live.sum())
@@ -134,14 +134,15 @@ def _reference(h, w, t, scale, mean=True):
     u = torch.finfo(kind).eps / 2
     acc = 2.0 ** -23
     zmax = float(z.abs().max()) if n else 0.0
-    e = float(2 * (d / 16 + 16) * acc * a + zmax * 2.0 ** -21 + 2.0 ** -20 + v * 2.0 ** -30)
+    e = 2 * (d / 16 + 16) * acc * a + zmax * 2.0 ** -21 + 2.0 ** -20 + v * 2.0 ** -30
     small = 2.0 ** -40 * g if kind == torch.float16 else 0.0
     least = 2.0 ** -25 if kind == torch.float16 else 0.0
     dh, dw = dz @ W, dz.t() @ H
     tol_dh = (dz.abs() @ W.abs()) * (u + 2 * e + (v / 16 + 64) * acc) + u * dh.abs() * 1.01 + least + small * W.abs().sum(0)
     tol_dw = (dz.abs().t() @ H.abs()) * (u + 2 * e + (n / 16 + 64) * acc) + u * dw.abs() * 1.01 + least + \
         small * H.abs().sum(0)
-    return dict(loss=loss.sum() / by, token_loss=loss, lse=lse, n=k, dh=dh, dw=dw, e=e, tol_dh=tol_dh, tol_dw=tol_dw)
+    return dict(loss=loss.sum() / by, token_loss=loss, lse=lse, n=k, dh=dh, dw=dw, e=e, tol_dh=tol_dh, tol_dw=tol_dw,
+                rows=1 if mean else k)
 
 
 def _close(got, want, tol, what):
@@ -153,8 +154,8 @@ def _check(r, ref):
     e = ref["e"]
     _close(r.lse, ref["lse"], e + ref["lse"].abs() * 2.0 ** -23, "lse")
     _close(r.token_loss, ref["token_loss"], 2 * e + ref["token_loss"].abs() * 2.0 ** -23, "token_loss")
-    _close(r.loss, ref["loss"], (2 * e + ref["loss"].abs() * 2.0 ** -23) * max(1.0, ref["n"] * 1.0
-                                                                             if ref["loss"] > 1e6 else 1.0), "loss")
+    # a mean is off by no more than its rows, a sum by all of them together
+    _close(r.loss, ref["loss"], ref["rows"] * 2 * e + ref["loss"].abs() * 2.0 ** -22, "loss")
     assert r.n_valid.item() == ref["n"]
     if isinstance(r, lsf.XentGrad):
         if r.grad_hidden is not None:
@@ -178,3 +179,330 @@ def test_loss_and_gradients_match_the_definition(shape, kind):
     ref = _reference(h, w, t, scale)
     _check(lsf.xent_loss(h, w, t), ref)
     _check(lsf.xent_grad(h, w, t, scale=scale), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_sum_int32_targets_and_one_gradient_at_a_time(n):
+    import torch
+    h, w, t = _inputs(n, 500, 128, "float16", 5)
+    ref = _reference(h, w, t, 4.0, mean=False)
+    t32 = t.to(torch.int32)
+    _check(lsf.xent_loss(h, w, t32, reduction="sum"), ref)
+    r = lsf.xent_grad(h, w, t32, scale=4.0, reduction="sum", grad_weight=None)
+    assert r.grad_weight is None
+    _check(r, ref)
+    r = lsf.xent_grad(h, w, t32, scale=4.0, reduction="sum", grad_hidden=False)
+    assert r.grad_hidden is None
+    _check(r, ref)
+    r = lsf.xent_grad(h, w, t32, scale=4.0, reduction="sum", grad_hidden=None, grad_weight=None)
+    assert r.grad_hidden is None and r.grad_weight is None
+    _check(r, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["float16", "bfloat16"])
+def test_several_pieces_and_cut_sums(kind):
+    """dz of 4000 x 40000 takes two pieces of the vocabulary, the second one
+    short; 200 x 40000 one piece with dH's sum cut in parts."""
+    for n, v, d in ((4000, 40000, 64), (200, 40001, 136)):
+        h, w, t = _inputs(n, v, d, kind, 6)
+        scale = 16.0 * n if kind == "float16" else 1.0
+        _check(lsf.xent_grad(h, w, t, scale=scale), _reference(h, w, t, scale))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 50, 200])
+def test_rows_with_gaps_and_unaligned_gradients(n):
+    import torch
+    v, d = 700, 200
+    h0, w0, t = _inputs(n, v, d, "float16", 7)
+    scale = 16.0 * n
+    ref = _reference(h0, w0, t, scale)
+
+    def gap(x, ld, shift=0):
+        room = torch.full((x.shape[0] * ld + 64,), 3.0, dtype=x.dtype, device="cuda")
+        out = room[shift:shift + x.shape[0] * ld].view(x.shape[0], ld)[:, :d]
+        out.copy_(x)
+        return out, room
+    h, _ = gap(h0, 264)
+    w, _ = gap(w0, 208)
+    for ld, shift in ((d, 0), (d + 8, 8), (d + 1, 0), (d + 8, 1), (d + 3, 5)):
+        gh, room_h = gap(h0, ld, shift)
+        gw, room_w = gap(w0, ld, shift)
+        r = lsf.xent_grad(h, w, t, scale=scale, grad_hidden=gh, grad_weight=gw)
+        assert r.grad_hidden is gh and r.grad_weight is gw
+        _check(r, ref)
+        for room, rows in ((room_h, n), (room_w, v)):      # nothing beside the rows is written
+            keep = torch.ones_like(room, dtype=torch.bool)
+            keep[shift:shift + rows * ld].view(rows, ld)[:, :d] = False
+            assert bool((room[keep] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 4, 60, 300])
+def test_nothing_left_to_learn(n):
+    """Every row ignored; no row at all."""
+    import torch
+    h, w, t = _inputs(n, 333, 72, "float16", 8)
+    t.fill_(IGNORE)
+    r = lsf.xent_grad(h, w, t, scale=1024.0)
+    assert r.loss.item() == 0.0 and r.n_valid.item() == 0
+    assert not r.token_loss.any() and not r.grad_hidden.any() and not r.grad_weight.any()
+    ref = _reference(h, w, t, 1.0)
+    _close(r.lse, ref["lse"], ref["e"] + ref["lse"].abs() * 2.0 ** -23, "lse")
+    r = lsf.xent_grad(h[:0], w, t[:0], scale=2.0, grad_weight=torch.ones_like(w))
+    assert r.loss.item() == 0.0 and r.n_valid.item() == 0 and r.grad_hidden.shape == (0, 72)
+    assert not r.grad_weight.any()
+    r = lsf.xent_loss(h[:0], w, t[:0])
+    assert r.loss.item() == 0.0 and r.token_loss.numel() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 50, 300])
+@pytest.mark.parametrize("bad", [-1, 1000, 1 << 40, -(1 << 62)])
+def test_a_target_that_is_no_class_poisons_the_result(n, bad):
+    import torch
+    h, w, t = _inputs(n, 1000, 64, "float16", 9, ignored=0.0)
+    t[n // 2] = bad
+    r = lsf.xent_grad(h, w, t)
+    assert math.isnan(r.loss.item()) and r.n_valid.item() == n
+    nan = torch.isnan(r.token_loss)
+    assert nan[n // 2] and int(nan.sum()) == 1
+    assert bool(torch.isnan(r.grad_hidden[n // 2]).all()) and bool(torch.isnan(r.grad_weight).all())
+    assert not bool(torch.isnan(r.grad_hidden[:n // 2]).any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 4, 100, 260])
+def test_an_ignored_index_that_is_a_class(n):
+    import torch
+    h, w, t = _inputs(n, 64, 64, "bfloat16", 10, ignored=0.0)
+    t[:] = torch.arange(n, device="cuda") % 3
+    ref = _reference(h, w, torch.where(t == 1, IGNORE, t), 1.0)
+    _check(lsf.xent_grad(h, w, t, ignore_index=1), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 90, 300])
+def test_extreme_logits(n):
+    """Logits of some thousands (nothing overflows), and a class that every row
+    excludes: a weight row that makes its logit -inf."""
+    import torch
+    h, w, t = _inputs(n, 600, 64, "bfloat16", 11, ignored=0.0, sure=0.0, std=100.0)
+    r = lsf.xent_loss(h, w, t)
+    _check(r, _reference(h, w, t, 1.0))
+    assert float(r.token_loss.max()) > 1000.0
+    h, w, t = _inputs(n, 600, 64, "float16", 12, ignored=0.0)
+    h[:, 0] = 1.0
+    w[7] = 0.0
+    w[7, 0] = -math.inf
+    t[t == 7] = 8
+    keep = torch.arange(600, device="cuda") != 7
+    ref = _reference(h, w[keep], t - (t > 7).long(), 1.0)
+    _check(lsf.xent_loss(h, w, t), ref)
+    t[0] = 7                                      # and one row whose target it is
+    assert lsf.xent_loss(h, w, t).token_loss[0].item() == math.inf
+    # rows that are nothing but -inf, and NaN in a row: NaN, there alone
+    w[:] = 0.0
+    w[:, 0] = -math.inf
+    assert math.isnan(lsf.xent_loss(h, w, t).token_loss[0].item())
+    h, w, t = _inputs(n, 600, 64, "float16", 13, ignored=0.0)
+    h[1, 5] = math.nan
+    r = lsf.xent_loss(h, w, t)
+    assert math.isnan(r.token_loss[1].item()) and int(torch.isnan(r.token_loss).sum()) == 1
+
+
+@pytest.mark.gpu
+def test_small_probabilities_survive_binary16():
+    """dz below binary16's range times S / n: rows with 2^-24-sized
+    probabilities still pull their weight."""
+    import torch
+    n, v, d = 256, 300, 64
+    h, w, t = _inputs(n, v, d, "float16", 14, ignored=0.0, sure=0.0, std=0.01)
+    h[:, 0] = 4.0
+    w[:, 0] = -1.0
+    w[:5, 0] = 3.0                                # the other 295 classes: exp(-16) = 1e-7 each
+    t[:] = torch.arange(n, device="cuda") % 5
+    ref = _reference(h, w, t, 2.0 ** 14)
+    r = lsf.xent_grad(h, w, t, scale=2.0 ** 14)
+    _check(r, ref)
+    tail = ref["dw"][5:, 0]
+    assert float(tail.abs().min()) > 0 and bool((r.grad_weight[5:, 0] != 0).all())
+    assert bool(((r.grad_weight[5:, 0].double() - tail).abs() <= 0.01 * tail.abs() + 2.0 ** -24).all())
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """Directional differences of the binary64 loss: exact to about
+    eps^2 |third derivative| (1e-8 here); the gradients' own tolerance is
+    what a direction can gather."""
+    import torch
+    h, w, t = _inputs(40, 200, 64, "bfloat16", 15)
+    ref = _reference(h, w, t, 1.0)
+    r = lsf.xent_grad(h, w, t)
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def loss(H, W):
+        live = t != IGNORE
+        z = H @ W.t()
+        return (torch.logsumexp(z, 1) - z.gather(1, torch.where(live, t, 0)[:, None])[:, 0])[live].mean()
+    H, W, eps = h.double(), w.double(), 1e-4
+    for x, grad, tol in ((H, r.grad_hidden, ref["tol_dh"]), (W, r.grad_weight, ref["tol_dw"])):
+        for _ in range(5):
+            d = torch.randn(x.shape, generator=g, device="cuda", dtype=torch.float64)
+            diff = (loss(H + eps * d, W) - loss(H - eps * d, W)) if x is H else (loss(H, W + eps * d) - loss(H, W - eps * d))
+            assert abs(float(diff / (2 * eps) - (grad.double() * d).sum())) <= float((tol * d.abs()).sum()) + 1e-6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [4, 100, 700])
+def test_same_bits_each_time_on_streams_and_in_graphs(n):
+    import torch
+    v, d = 9000, 192
+    h, w, t = _inputs(n, v, d, "float16", 16)
+    S = torch.full((1,), 64.0, device="cuda")
+    first = lsf.xent_grad(h, w, t, scale=S)
+
+    def same(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+    # two calls at once, on streams of their own
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    rs = []
+    for k in range(6):
+        with torch.cuda.stream(streams[k % 2]):
+            rs.append(lsf.xent_grad(h, w, t, scale=S))
+    rs.append(lsf.xent_grad(h, w, t, scale=S, stream=streams[0]))
+    torch.cuda.synchronize()
+    assert all(same(first, r) for r in rs)
+    # captured, replayed on other inputs and another S
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        r = lsf.xent_grad(h, w, t, scale=S)
+    h2, w2, t2 = _inputs(n, v, d, "float16", 17)
+    h.copy_(h2)
+    w.copy_(w2)
+    t.copy_(t2)
+    S.fill_(256.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert same(r, lsf.xent_grad(h2, w2, t2, scale=256.0))
+    _check(r, _reference(h2, w2, t2, 256.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 40])
+def test_offsets_beyond_31_bits(n):
+    """A head of 2.2e9 values: its last rows are read and written."""
+    import torch
+    v, d = 270_000, 8192
+    w = torch.zeros(v, d, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w[-2000:] = torch.randn(2000, d, generator=g, device="cuda").mul_(0.02).bfloat16()
+    h = torch.randn(n, d, generator=g, device="cuda").bfloat16()
+    t = torch.arange(v - n, v, device="cuda")
+    r = lsf.xent_grad(h, w, t)
+    H, W = h.double(), w[-2000:].double()
+    z = H @ W.t()                                   # the other 268000 logits are 0
+    lse = torch.logaddexp(torch.logsumexp(z, 1), torch.tensor(math.log(v - 2000.0), device="cuda"))
+    loss = lse - z[:, -n:].diagonal()
+    # e as above with A <= |h| |w| (Cauchy-Schwarz), max|z| <= 12
+    e = 2 * (d / 16 + 16) * 2.0 ** -23 * float(H.norm(dim=1).max() * W.norm(dim=1).max()) + 12 * 2.0 ** -21 + \
+        2.0 ** -20 + v * 2.0 ** -30
+    _close(r.token_loss, loss, 2 * e + loss * 2.0 ** -23, "token_loss")
+    dz = torch.exp(z - lse[:, None])
+    dz[torch.arange(n, device="cuda"), torch.arange(2000 - n, 2000, device="cuda")] -= 1.0
+    dz /= n
+    u = 2.0 ** -8
+    tol = (dz.abs().t() @ H.abs()) * (u + 2 * e + 66 * 2.0 ** -23) + u * 1.01 * (dz.t() @ H).abs()
+    _close(r.grad_weight[-2000:], dz.t() @ H, tol, "grad_weight")
+    want = dz @ W
+    _close(r.grad_hidden, want, (dz.abs() @ W.abs()) * (u + 2 * e + (v / 16 + 64) * 2.0 ** -23) + u * 1.01 * want.abs(),
+           "grad_hidden")
+
+
+def test_refusals_of_the_binding_on_the_cpu():
+    import torch
+    h, w, t = torch.zeros(4, 16).half(), torch.zeros(8, 16).half(), torch.zeros(4, dtype=torch.int64)
+    for fn in (lsf.xent_loss, lsf.xent_grad):
+        with pytest.raises(ValueError):
+            fn(h, w, t)
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_binding():
+    import torch
+    h, w, t = _inputs(10, 50, 64, "float16", 18)
+    good = dict(hidden=h, weight=w, targets=t)
+    for kw in (dict(hidden=h.float()), dict(weight=w.bfloat16()), dict(hidden=h[None]), dict(weight=w[:, :32]),
+               dict(hidden=h.t()), dict(targets=t[:9]), dict(targets=t.float()), dict(targets=t.cpu()),
+               dict(targets=torch.stack([t, t], 1)[:, 0]), dict(weight=w.cpu()), dict(hidden=h.float(), weight=w.float()),
+               dict(reduction="none")):
+        with pytest.raises(ValueError):
+            lsf.xent_loss(**(good | kw))
+    for kw in (dict(grad_hidden=torch.zeros_like(h)[:5]), dict(grad_weight=torch.zeros(50, 64, device="cuda")),
+               dict(grad_weight=torch.zeros_like(w).cpu()), dict(scale=torch.ones(2, device="cuda")),
+               dict(scale=torch.ones(1))):
+        with pytest.raises(ValueError):
+            lsf.xent_grad(**(good | kw))
+    for kw in (dict(hidden=torch.zeros(10, 60, device="cuda").half(), weight=torch.zeros(50, 60, device="cuda").half()),
+               dict(hidden=torch.zeros(10, 65, device="cuda").half()[:, 1:]), dict(scale=0.0), dict(scale=math.inf),
+               dict(grad_hidden=h), dict(grad_weight=w)):
+        with pytest.raises(lsf.MptError) as e:
+            lsf.xent_grad(**(good | kw))
+        assert e.value.code == lsf.MPT_ERR_INVALID_ARG, kw
+    _check(lsf.xent_grad(**good), _reference(h, w, t, 1.0))     # and the good call still works
+
+
+# ---------------------------------------------------------------------------
+# the operators together, as a training step uses them
+# ---------------------------------------------------------------------------
+
+@pytest.mark.gpu
+def test_head_loss_norm_and_step_together():
+    """Loss and gradients from the handle's FP16 copy and device scale, the
+    norm of the gradients, the step; then an S that overflows FP16 makes the
+    gradients inf, the list finds it, and the step skips and halves S."""
+    import torch
+    v, d, n = 1000, 128, 200
+    h, w0, t = _inputs(n, v, d, "float16", 19)
+    opt = lsf.MPT([v * d, d], lsf.Config())
+    opt.master(0).copy_(w0.float().flatten())
+    opt.refresh_half()
+    opt.set_scaler_state(2.0 ** 12)
+    grads = [torch.zeros(v * d, dtype=torch.float16, device="cuda"),
+             torch.full((d,), 0.25, dtype=torch.float16, device="cuda")]
+    lst = lsf.GradList([v * d, d], torch.float16)
+    assert torch.equal(opt.w16(0), w0.flatten())
+    r = opt.head_grad(0, h, t, grad_weight=grads[0].view(v, d))
+    norms = lst.norm(grads, scale=opt.device_scale(), tensor_norms=True)
+    opt.step_async(grads, 0.5, 0.0, 0.0)
+    res = opt.wait()
+    ref = _reference(h, w0, t, 2.0 ** 12)
+    _check(r, ref)
+    assert res["found_inf"] == 0
+    got = norms["norm"].item()
+    assert abs(got - res["grad_norm"]) <= 1e-12 * got
+    assert abs(norms["tensor_norms"][0].item() - float(ref["dw"].norm()) / 2 ** 12) <= float(ref["tol_dw"].norm()) / 2 ** 12
+    # the step took this gradient: w - lr g, one rounding each
+    want = w0.double().flatten() - 0.5 * grads[0].double() / 2 ** 12
+    assert bool(((opt.master(0).double() - want).abs() <= want.abs() * 2.0 ** -23 + 1e-12).all())
+    # the loss at the new weights is that of the new FP16 copy
+    r2 = opt.head_grad(0, h, t, grad_weight=grads[0].view(v, d))
+    _check(r2, _reference(h, opt.w16(0).view(v, d), t, 2.0 ** 12))
+    # overflow: dW of some class is about S / n * sum of its rows' hidden
+    opt.set_scaler_state(2.0 ** 23)
+    before = opt.master(0).clone()
+    r = opt.head_grad(0, h, t, grad_weight=grads[0].view(v, d))
+    assert math.isfinite(r.loss.item())
+    found = lst.norm(grads, scale=opt.device_scale())
+    opt.step_async(grads, 0.5, 0.0, 0.0)
+    res = opt.wait()
+    assert res["found_inf"] == 1 and res["new_scale"] == 2.0 ** 22 and found["found_inf"].item() == 1
+    assert found["n_nonfinite"].item() == res["n_nonfinite"] > 0
+    assert torch.equal(opt.master(0), before)
+    with pytest.raises(ValueError):
+        opt.head_grad(0, h[:, :120], t)
+    opt.close()
