@@ -531,10 +531,11 @@ int mpt_xent_args_init(mpt_xent_args* args);
 int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes);
 
 /* Queue the loss and the gradients asked for on cuda_stream and return.  All
- * pointers are device pointers of the current device; gradients may not touch
- * hidden, weight or each other.  The workspace (256-byte aligned) holds
- * nothing between calls: calls that may overlap on the GPU need one each.
- * Can be captured into a CUDA graph.
+ * pointers are device pointers of the current device; the address ranges of
+ * the gradients may not meet those of hidden, weight or each other.  The
+ * workspace (256-byte aligned) holds nothing between calls: calls that may
+ * overlap on the GPU need one each.  Can be captured into a CUDA graph; the
+ * first call on a device loads the kernels, so make one before any capture.
  * Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA; on an
  * argument error nothing is queued. */
 int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void* cuda_stream);

@@ -415,6 +415,14 @@ def _scale_args(scale, device):
     return float(scale), None
 
 
+def _used_on(stream, *tensors):
+    """Tell the allocator that ``stream`` reads or writes these tensors."""
+    import torch
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+
+
 class GradList:
     """Global gradient norm over a fixed list of tensors, and clipping
     (``mpt_list_*``): FP16, BF16 or FP32 tensors, one type for all or one each.
@@ -490,8 +498,11 @@ class GradList:
         """Queue the norm of ``grads`` (CUDA tensors, or an array from
         :func:`grad_pointers`); ``clip`` only sets the ``coef`` reported."""
         host, dev = _scale_args(scale, self.device)
+        g = self._ptrs(grads, self.dtypes, "gradient")
+        if stream is not None:
+            _used_on(stream, scale, *(() if g is grads else grads))
         with _on(self.device, stream):
-            _check(lib().mpt_list_norm(self._h, self._ptrs(grads, self.dtypes, "gradient"), host, dev, clip,
+            _check(lib().mpt_list_norm(self._h, g, host, dev, clip,
                                        MPT_LIST_TENSOR_NORMS if tensor_norms else 0,
                                        _stream_ptr(stream, self.device)), "mpt_list_norm")
         return self._views(tensor_norms)
@@ -504,6 +515,8 @@ class GradList:
         if out is None and self.out_dtypes != self.dtypes:
             raise ValueError("outputs of another type need tensors of their own")
         o = g if out is None else self._ptrs(out, self.out_dtypes, "output")
+        if stream is not None:
+            _used_on(stream, scale, *(() if g is grads else grads), *(() if out is None or o is out else out))
         flags = (MPT_LIST_TENSOR_NORMS if tensor_norms else 0) | (MPT_LIST_UNSCALE if unscale else 0)
         with _on(self.device, stream):
             _check(lib().mpt_list_clip(self._h, g, o, host, dev, clip, flags,
@@ -562,6 +575,8 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
     if reduction not in ("mean", "sum"):
         raise ValueError("reduction is 'mean' or 'sum'")
     host_scale, dev_scale = _scale_args(scale, dev)
+    if stream is not None:
+        _used_on(stream, hidden, weight, targets, scale, grad_hidden, grad_weight)
     # what the call allocates belongs to the stream that it runs on
     with _on(dev, stream):
         f32 = torch.float32

@@ -1233,6 +1233,8 @@ bool args_ok(const mpt_xent_args* a)
     if (a->reduction != MPT_XENT_MEAN && a->reduction != MPT_XENT_SUM)
         return false;
     // tiles are counted in 31 bits
+    if (a->n * a->d >= (int64_t)1 << 38)  // strides of tensor maps have 40 bits
+        return false;
     const int64_t most = (int64_t)1 << 30, rows = ceil_div(a->n, kRows), wide = ceil_div(a->d, kTileN);
     return rows * ceil_div(a->v, kTileN) <= most && rows * wide * 64 <= most && ceil_div(a->v, kRows) * wide <= most;
 }
@@ -1250,7 +1252,7 @@ bool meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 bool pointers_ok(const mpt_xent_args& a)
 {
-    const int64_t big = (int64_t)1 << 40;
+    const int64_t big = (int64_t)1 << 39;
     auto rows = [&](const void* p, int64_t ld, uintptr_t align, int64_t quantum) {
         return p && reinterpret_cast<uintptr_t>(p) % align == 0 && ld >= a.d && ld < big && ld % quantum == 0;
     };
@@ -1313,31 +1315,52 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t co
                     box_rows);
 }
 
-// Lets a kernel use `bytes` of shared memory, once per device; a failure is
-// not remembered.
 template <class K>
-cudaError_t allow_smem(std::atomic<uint64_t>& set_up, K kernel, int bytes)
+bool allow_smem(K kernel, int bytes)
 {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+template <bool kPair, int kMode, bool kBf16>
+bool allow_product()
+{
+    return allow_smem(xent_product_kernel<kPair, kMode, kBf16>, Shape<kPair, kMode>::kSmem);
+}
+
+template <bool kBf16>
+bool load_kernels()
+{
+    cudaFuncAttributes fa;
+    return allow_product<false, kLoss, kBf16>() && allow_product<true, kLoss, kBf16>() &&
+           allow_product<false, kDz, kBf16>() && allow_product<true, kDz, kBf16>() &&
+           allow_product<false, kGrad, kBf16>() && allow_product<true, kGrad, kBf16>() &&
+           allow_smem(xent_few_kernel<kBf16, 1>, kFewSmem) && allow_smem(xent_few_kernel<kBf16, 2>, kFewSmem) &&
+           allow_smem(xent_few_kernel<kBf16, kFew>, kFewSmem) &&
+           cudaFuncGetAttributes(&fa, xent_merge_kernel<kBf16>) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, xent_dh_kernel<kBf16>) == cudaSuccess;
+}
+
+// Once per device, at its first call: every kernel is loaded and may use its
+// shared memory, so that no later call loads code inside a capture.  A failure
+// is not remembered.
+bool set_up_device()
+{
+    static std::atomic<uint64_t> done{0};
     int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return false;
     const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-    if (set_up.load(std::memory_order_acquire) & bit)
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        set_up.fetch_or(bit, std::memory_order_release);
-    return e;
+    if (done.load(std::memory_order_acquire) & bit)
+        return true;
+    if (!encode_fn() || !load_kernels<false>() || !load_kernels<true>())
+        return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
 }
 
 template <bool kBf16, int kN>
 cudaError_t launch_few(const GemmArgs& g, const mpt_xent_args& a, const Plan& p, cudaStream_t st)
 {
-    static std::atomic<uint64_t> set_up{0};
-    const cudaError_t e = allow_smem(set_up, xent_few_kernel<kBf16, kN>, kFewSmem);
-    if (e != cudaSuccess)
-        return e;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)p.parts);
     lc.blockDim = dim3(kFewThreads);
@@ -1351,10 +1374,6 @@ template <bool kPair, int kMode, bool kBf16>
 cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
 {
     using S = Shape<kPair, kMode>;
-    static std::atomic<uint64_t> set_up{0};
-    const cudaError_t e = allow_smem(set_up, xent_product_kernel<kPair, kMode, kBf16>, S::kSmem);
-    if (e != cudaSuccess)
-        return e;
     cudaLaunchConfig_t lc = {};
     const int32_t tiles = g.job[0].tiles + g.job[1].tiles;
     const int32_t workers = std::min(tiles, kMaxCtas / S::kCtas);
@@ -1587,6 +1606,10 @@ int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void
         return rc;
     if (!d_workspace || reinterpret_cast<uintptr_t>(d_workspace) % kAlign != 0 || ws_bytes < p.total)
         return MPT_ERR_WORKSPACE;
+    if (!set_up_device()) {
+        cudaGetLastError();
+        return MPT_ERR_CUDA;
+    }
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     char* ws = static_cast<char*>(d_workspace);
     const int done = args->type == MPT_BF16 ? enqueue<true>(*args, p, ws, st) : enqueue<false>(*args, p, ws, st);
