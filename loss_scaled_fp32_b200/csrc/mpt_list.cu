@@ -37,7 +37,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kGranule = 512;      // bytes: one 16-byte load per lane
+constexpr int kGranule = 1024;     // bytes: one 32-byte load per lane
 constexpr int kPtrSlots = 4;       // pointer tables held on the device at once
 constexpr int kLongRuns = 128;
 constexpr size_t kAlign = 256;
@@ -104,20 +104,51 @@ template <> struct Elem<MPT_F32> {
     static __device__ __forceinline__ T down(float x) { return x; }
 };
 
-// The 16 bytes of one load as binary32 values.
-template <int kType>
-__device__ __forceinline__ void widen(const uint4& v, float* x)
+// One load or store of a lane: 32 bytes, the memory's own unit.  (Stores of 16
+// bytes, two to a unit, took 48 us for the clipping of 25M FP16 gradients into FP32,
+// 32 bytes at once take 39.)
+struct Vec {
+    uint32_t w[8];
+};
+constexpr int kVec = (int)sizeof(Vec);
+
+// kOnce: nothing writes there while the kernel runs.
+template <bool kOnce>
+__device__ __forceinline__ Vec load_vec(const void* p)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    Vec v;
+    if constexpr (kOnce)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                     : "l"(p)
+                     : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_vec(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The 32 bytes of one load as binary32 values.
+template <int kType>
+__device__ __forceinline__ void widen(const Vec& v, float* x)
+{
     if constexpr (kType == MPT_F32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            x[k] = __uint_as_float(w[k]);
+        for (int k = 0; k < 8; ++k)
+            x[k] = __uint_as_float(v.w[k]);
     } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[2 * k] = Elem<kType>::up((uint16_t)(w[k] & 0xFFFFu));
-            x[2 * k + 1] = Elem<kType>::up((uint16_t)(w[k] >> 16));
+        for (int k = 0; k < 8; ++k) {
+            x[2 * k] = Elem<kType>::up((uint16_t)(v.w[k] & 0xFFFFu));
+            x[2 * k + 1] = Elem<kType>::up((uint16_t)(v.w[k] >> 16));
         }
     }
 }
@@ -134,53 +165,51 @@ __device__ __forceinline__ double warp_sum(double x)
 // the norm pass
 // ---------------------------------------------------------------------------
 
-// Sum of squares of one run by one warp.  Eight 16-byte loads are in flight
-// per lane; elements before the first 16-byte boundary and after the last go
+// Sum of squares of one run by one warp.  Four 32-byte loads are in flight
+// per lane; elements before the first 32-byte boundary and after the last go
 // one to a lane.
 template <int kType>
 __device__ __forceinline__ double run_square(const void* base, int64_t begin, int64_t len, int lane)
 {
     using T = typename Elem<kType>::T;
-    constexpr int kPer = 16 / (int)sizeof(T);
-    constexpr int kU = 8;
+    constexpr int kPer = kVec / (int)sizeof(T);
+    constexpr int kU = 4;
     const T* g = static_cast<const T*>(base) + begin;
-    const int skew = (int)(reinterpret_cast<uintptr_t>(g) & 15) / (int)sizeof(T);
+    const int skew = (int)(reinterpret_cast<uintptr_t>(g) & (kVec - 1)) / (int)sizeof(T);
     const int64_t head = min(len, (int64_t)((kPer - skew) % kPer));
     const int64_t nv = (len - head) / kPer;
-    const uint4* v = reinterpret_cast<const uint4*>(g + head);
+    const Vec* v = reinterpret_cast<const Vec*>(g + head);
     double a0 = 0.0, a1 = 0.0;
+    auto add = [&](const Vec& q) {
+        float x[kPer];
+        widen<kType>(q, x);
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+            a0 = fma((double)x[e], (double)x[e], a0);
+            a1 = fma((double)x[e + 1], (double)x[e + 1], a1);
+        }
+    };
     int64_t i = lane;
     for (; i + (kU - 1) * 32 < nv; i += kU * 32) {
-        uint4 q[kU];
+        Vec q[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k)
-            q[k] = __ldg(v + i + k * 32);
+            q[k] = load_vec<true>(v + i + k * 32);
 #pragma unroll
-        for (int k = 0; k < kU; ++k) {
-            float x[kPer];
-            widen<kType>(q[k], x);
-#pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                a0 = fma((double)x[e], (double)x[e], a0);
-                a1 = fma((double)x[e + 1], (double)x[e + 1], a1);
-            }
-        }
+        for (int k = 0; k < kU; ++k)
+            add(q[k]);
     }
     if (i - lane < nv) {  // the last, partly filled batch in one round, too
-        uint4 q[kU];
-#pragma unroll
-        for (int k = 0; k < kU; ++k)
-            q[k] = i + k * 32 < nv ? __ldg(v + i + k * 32) : make_uint4(0, 0, 0, 0);
+        Vec q[kU];
 #pragma unroll
         for (int k = 0; k < kU; ++k) {
-            float x[kPer];
-            widen<kType>(q[k], x);
-#pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                a0 = fma((double)x[e], (double)x[e], a0);
-                a1 = fma((double)x[e + 1], (double)x[e + 1], a1);
-            }
+            q[k] = Vec{};
+            if (i + k * 32 < nv)
+                q[k] = load_vec<true>(v + i + k * 32);
         }
+#pragma unroll
+        for (int k = 0; k < kU; ++k)
+            add(q[k]);
     }
     if (lane < head) {
         const double x = (double)Elem<kType>::up(g[lane]);
@@ -392,18 +421,21 @@ __device__ __forceinline__ typename Elem<kOut>::T scaled(float x, float inv, flo
     return Elem<kOut>::down(__fmul_rn(x, coef));
 }
 
-// One batch of kN 16-byte input vectors, 32 lanes apart, scaled and stored;
+// One batch of kN 32-byte input vectors, 32 lanes apart, scaled and stored;
 // kEnds: those from `end` on are left out.
 template <int kIn, int kOut, int kN, bool kEnds>
-__device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::T* o, int64_t i, int64_t end,
+__device__ __forceinline__ void scale_vecs(const Vec* v, typename Elem<kOut>::T* o, int64_t i, int64_t end,
                                            bool wide, float inv, float coef, bool unscale)
 {
     using TO = typename Elem<kOut>::T;
-    constexpr int kPer = 16 / (int)sizeof(typename Elem<kIn>::T);
-    uint4 q[kN];
+    constexpr int kPer = kVec / (int)sizeof(typename Elem<kIn>::T);
+    Vec q[kN];
 #pragma unroll
-    for (int k = 0; k < kN; ++k)
-        q[k] = !kEnds || i + k * 32 < end ? v[i + k * 32] : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kN; ++k) {
+        q[k] = Vec{};
+        if (!kEnds || i + k * 32 < end)
+            q[k] = load_vec<false>(v + i + k * 32);
+    }
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
         const bool in = !kEnds || i + k * 32 < end;
@@ -415,24 +447,22 @@ __device__ __forceinline__ void scale_vecs(const uint4* v, typename Elem<kOut>::
             y[e] = scaled<kIn, kOut>(x[e], inv, coef, unscale);
         TO* to = o + (i + k * 32) * kPer;
         if (in && wide) {
-            // kPer outputs are 8, 16 or 32 bytes
-            constexpr int kBytes = kPer * (int)sizeof(TO);
-            uint32_t w[kBytes / 4];
-            if constexpr (sizeof(TO) == 4) {
+            // kPer outputs are 16, 32 or 64 bytes
+            constexpr int kWords = kPer * (int)sizeof(TO) / 4;
+            uint32_t w[kWords];
 #pragma unroll
-                for (int e = 0; e < kPer; ++e)
+            for (int e = 0; e < kWords; ++e) {
+                if constexpr (sizeof(TO) == 4)
                     w[e] = __float_as_uint(y[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kPer / 2; ++e)
+                else
                     w[e] = (uint32_t)y[2 * e] | ((uint32_t)y[2 * e + 1] << 16);
             }
-            if constexpr (kBytes == 8) {
-                *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+            if constexpr (kWords == 4) {
+                *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
-                for (int e = 0; e < kBytes / 16; ++e)
-                    reinterpret_cast<uint4*>(to)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                for (int e = 0; e < kWords; e += 8)
+                    store_vec(reinterpret_cast<uint32_t*>(to) + e, w + e);
             }
         } else if (in) {
 #pragma unroll
@@ -450,17 +480,17 @@ __device__ __forceinline__ void run_scale(const void* base, void* out, int64_t b
 {
     using T = typename Elem<kIn>::T;
     using TO = typename Elem<kOut>::T;
-    constexpr int kPer = 16 / (int)sizeof(T);
-    constexpr int kU = 4;
+    constexpr int kPer = kVec / (int)sizeof(T);
+    constexpr int kU = 2;
     const T* g = static_cast<const T*>(base) + begin;
     TO* o = static_cast<TO*>(out) + begin;
-    const int skew = (int)(reinterpret_cast<uintptr_t>(g) & 15) / (int)sizeof(T);
+    const int skew = (int)(reinterpret_cast<uintptr_t>(g) & (kVec - 1)) / (int)sizeof(T);
     const int64_t head = min(len, (int64_t)((kPer - skew) % kPer));
     const int64_t nv = (len - head) / kPer;
     const int64_t tail = head + nv * kPer;
-    const uint4* v = reinterpret_cast<const uint4*>(g + head);
+    const Vec* v = reinterpret_cast<const Vec*>(g + head);
     TO* ov = o + head;
-    constexpr int kOutAlign = kPer * (int)sizeof(TO) < 16 ? kPer * (int)sizeof(TO) : 16;
+    constexpr int kOutAlign = kPer * (int)sizeof(TO) < kVec ? kPer * (int)sizeof(TO) : kVec;
     const bool wide = (reinterpret_cast<uintptr_t>(ov) & (kOutAlign - 1)) == 0;
     if (tail + lane < len)
         o[tail + lane] = scaled<kIn, kOut>(Elem<kIn>::up(g[tail + lane]), inv, coef, unscale);
@@ -571,9 +601,9 @@ int build_plan(const int64_t* sizes, const int32_t* types, const int32_t* out_ty
             return MPT_ERR_INVALID_ARG;
     }
     const int64_t warps_max = (int64_t)kMaxCtas * kWarps;
-    // at least 2 KB (four loads a lane) to a warp: a million FP16 values are done
+    // at least 2 KB (two loads a lane) to a warp: a million FP16 values are done
     // by 128 CTAs in 8.2 us, by 512 CTAs of a quarter of the work in 10.4 us
-    const int64_t warps_wanted = std::max<int64_t>(1, std::min((units + 3) / 4, warps_max));
+    const int64_t warps_wanted = std::max<int64_t>(1, std::min((units + 1) / 2, warps_max));
     p.ctas = (int32_t)((warps_wanted + kWarps - 1) / kWarps);
     const int64_t warps = (int64_t)p.ctas * kWarps;
     p.warp_runs.assign(1, 0);
