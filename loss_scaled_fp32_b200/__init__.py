@@ -579,9 +579,10 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
         _used_on(stream, hidden, weight, targets, scale, grad_hidden, grad_weight)
     # what the call allocates belongs to the stream that it runs on
     with _on(dev, stream):
-        f32 = torch.float32
-        loss, n_valid = hidden.new_empty(1, dtype=f32), targets.new_empty(1, dtype=torch.int64)
-        token_loss, lse = hidden.new_empty(n, dtype=f32), hidden.new_empty(n, dtype=f32)
+        # one allocation for the small results
+        n_valid, loss, _, token_loss, lse = torch.unsafe_split_with_sizes(
+            hidden.new_empty(4 + 2 * n, dtype=torch.float32), (2, 1, 1, n, n))
+        n_valid = n_valid.view(torch.int64)
         gh = gw = None
         ld_gh = ld_gw = 0
         if grad_hidden is not None and grad_hidden is not False:
