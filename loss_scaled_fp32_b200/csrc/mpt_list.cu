@@ -778,8 +778,10 @@ int find_slot(mpt_list* h, const void* const* grads, void* const* outs, cudaStre
         }
     }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &cap) != cudaSuccess)
-        return fail_cuda(h);
+    if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
+        cudaGetLastError();  // the default stream while another one is captured: nothing was queued
+        return MPT_ERR_CUDA;
+    }
     const bool capturing = cap != cudaStreamCaptureStatusNone;
     // a norm finds its gradients in a clipping's table too
     int k = -1;

@@ -924,16 +924,26 @@ constexpr int kMergeRows = 8;  // rows (warps) per CTA
 template <bool kBf16>
 __device__ __forceinline__ float target_logit(const uint16_t* h, const uint16_t* w, int d, int lane)
 {
+    constexpr int kU = 4;  // loads of either row under way
     float s0 = 0.0f, s1 = 0.0f;
-    for (int k = lane * 8; k < d; k += 256) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(h + k)), b = __ldg(reinterpret_cast<const uint4*>(w + k));
-        float x[8], y[8];
-        widen8<kBf16>(a, x);
-        widen8<kBf16>(b, y);
+    for (int k = lane * 8; k < d; k += kU * 256) {
+        uint4 a[kU], b[kU];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            s0 = fmaf(x[e], y[e], s0);
-            s1 = fmaf(x[e + 1], y[e + 1], s1);
+        for (int e = 0; e < kU; ++e) {
+            const bool in = k + e * 256 < d;
+            a[e] = in ? __ldg(reinterpret_cast<const uint4*>(h + k + e * 256)) : make_uint4(0, 0, 0, 0);
+            b[e] = in ? __ldg(reinterpret_cast<const uint4*>(w + k + e * 256)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < kU; ++e) {
+            float x[8], y[8];
+            widen8<kBf16>(a[e], x);
+            widen8<kBf16>(b[e], y);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                s0 = fmaf(x[i], y[i], s0);
+                s1 = fmaf(x[i + 1], y[i + 1], s1);
+            }
         }
     }
     float s = s0 + s1;
@@ -984,19 +994,20 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
         // maximum and sum of each lane's parts, then of the lanes'
         const float2* p = g.part + (int64_t)row * g.part_ld;
         float top = -INFINITY, sum = 0.0f;
-        for (int k = lane; k < g.part_ld; k += 32 * 8) {
-            float2 q[8];
+        constexpr int kU = 16;  // a vocabulary of 50257 in one round
+        for (int k = lane; k < g.part_ld; k += 32 * kU) {
+            float2 q[kU];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < kU; ++e)
                 q[e] = k + 32 * e < g.part_ld ? __ldcg(p + k + 32 * e) : make_float2(-INFINITY, 0.0f);
             float now = top;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < kU; ++e)
                 now = fmaxf(now, q[e].x);
             const float base = now == -INFINITY ? 0.0f : now;
             sum *= expf(top - base);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < kU; ++e)
                 sum += q[e].y * expf(q[e].x - base);
             top = now;
         }
@@ -1038,15 +1049,19 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
             m.loss += s_loss[k];
             m.valid += s_valid[k];
         }
+        s_last = 1;
         a.parts[blockIdx.x] = m;
-        __threadfence();
-        s_last = atomicAdd(&g.control->ticket, 1u) == gridDim.x - 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            s_last = atomicAdd(&g.control->ticket, 1u) == gridDim.x - 1;
+        }
         s_bad = 0;
     }
     __syncthreads();
     if (!s_last)
         return;
-    __threadfence();
+    if (gridDim.x > 1)
+        __threadfence();
     double sum = 0.0;
     unsigned long long count = 0;
     for (int k = threadIdx.x; k < (int)gridDim.x; k += kMergeRows * 32) {
