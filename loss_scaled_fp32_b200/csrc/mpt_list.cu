@@ -689,6 +689,7 @@ struct mpt_list {
     };
     Slot slot[kPtrSlots];
     uint64_t clock = 0;
+    int last_slot = 0;
     mpt_check_result* mailbox = nullptr;
     bool broken = false;
 };
@@ -766,33 +767,36 @@ int find_slot(mpt_list* h, const void* const* grads, void* const* outs, cudaStre
 {
     const int32_t n = h->n;
     const size_t half = sizeof(void*) * (size_t)n;
-    for (int32_t i = 0; i < n; ++i) {
-        if (h->sizes[i] == 0)
-            continue;
-        const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
-        if (g == 0 || g % type_bytes(h->types[i]))
-            return MPT_ERR_INVALID_ARG;
-        if (outs) {
-            const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
-            if (o == 0 || o % type_bytes(h->out_types[i]))
-                return MPT_ERR_INVALID_ARG;
-        }
-    }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
         cudaGetLastError();  // the default stream while another one is captured: nothing was queued
         return MPT_ERR_CUDA;
     }
     const bool capturing = cap != cudaStreamCaptureStatusNone;
-    // a norm finds its gradients in a clipping's table too
+    // a norm finds its gradients in a clipping's table too; the slot used last
+    // is looked at first
     int k = -1;
-    for (int i = 0; k < 0 && i < kPtrSlots; ++i) {
+    for (int j = 0; k < 0 && j < kPtrSlots; ++j) {
+        const int i = (h->last_slot + j) % kPtrSlots;
         const auto& s = h->slot[i];
         if (s.valid && (!outs || s.clip) && std::memcmp(s.ptrs.data(), grads, half) == 0 &&
             (!outs || std::memcmp(s.ptrs.data() + n, outs, half) == 0))
             k = i;
     }
     if (k < 0) {
+        // (a table that is held has passed these checks)
+        for (int32_t i = 0; i < n; ++i) {
+            if (h->sizes[i] == 0)
+                continue;
+            const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+            if (g == 0 || g % type_bytes(h->types[i]))
+                return MPT_ERR_INVALID_ARG;
+            if (outs) {
+                const uintptr_t o = reinterpret_cast<uintptr_t>(outs[i]);
+                if (o == 0 || o % type_bytes(h->out_types[i]))
+                    return MPT_ERR_INVALID_ARG;
+            }
+        }
         if (capturing)
             return MPT_ERR_INVALID_ARG;  // the copy of a new table must not be recorded
         for (int i = 0; i < kPtrSlots; ++i) {
@@ -828,6 +832,7 @@ int find_slot(mpt_list* h, const void* const* grads, void* const* outs, cudaStre
         s.valid = true;
     }
     h->slot[k].used = ++h->clock;
+    h->last_slot = k;
     if (capturing)
         h->slot[k].captured = true;
     *out = k;
