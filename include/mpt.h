@@ -479,7 +479,8 @@ int mpt_list_destroy(mpt_list* h);
  * The start of the backward pass: the loss that S multiplies.  For n rows of
  * hidden (n x d), a head's weight (v x d) and one target class per row,
  *
- *   z      = hidden weight^T                    (never stored)
+ *   z      = hidden weight^T        (no buffer grows to this size: at most
+ *                                    256 MB of it are held at once)
  *   loss_i = log(sum_u exp(z_iu)) - z_it        (0 where t == ignore_index)
  *   loss   = sum of loss_i, or that divided by the number of rows that are
  *            not ignored (MPT_XENT_MEAN; 0 where every row is)

@@ -605,7 +605,8 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
 
 def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stream=None):
     """Softmax cross entropy of ``hidden @ weight.T`` against ``targets``
-    (``mpt_xent`` without gradients), queued; the logits are not stored.
+    (``mpt_xent`` without gradients), queued; the logits are not stored (with
+    gradients, of at most 256 MB of them at a time).
 
     Returns ``XentLoss``: ``loss`` (float32, 1 value), ``token_loss`` and
     ``lse`` (float32, one per row), ``n_valid`` (int64, 1 value)."""

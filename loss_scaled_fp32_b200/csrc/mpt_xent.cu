@@ -6,11 +6,13 @@
 //   dz_iu  = exp(z_iu - lse_i) - [u = t]            (at u = t: expm1(-loss_i))
 //   dH = g dz W,  dW = g dz^T H,  g = S / valid rows (or S)
 //
-// The logits are never kept.  The forward pass reduces each 256-column tile of
-// z to a maximum and a sum per row while the next tile is multiplied; the
-// backward pass goes through the vocabulary in pieces: multiply z again, write
-// dz of the piece in 16 bits, and multiply it with W (dH, summed over the
-// pieces in binary32) and with H (this piece's rows of dW, final at once).
+// No buffer grows to the logits' size.  The forward pass reduces each
+// 256-column tile of z to a maximum and a sum per row while the next tile is
+// multiplied; the backward pass goes through the vocabulary in pieces: multiply
+// z again, write dz of the piece in 16 bits, and multiply it with W (dH, summed
+// over the pieces in binary32) and with H (this piece's rows of dW, final at
+// once).  Where all of a call's logits fit in a piece's buffer and moving them
+// is cheaper than multiplying again, they stay there between the passes.
 //
 // The loss is formed from the other columns' sum against the target's logit,
 // so a sure answer's small loss keeps its digits, and dz at the target comes
@@ -124,6 +126,8 @@ struct GemmArgs {
     float2* part;         // [n][part_ld]: maximum and sum of half a tile's columns
     int32_t part_ld;
     Control* control;
+    float* z;             // [n][z_ld]: the logits, where a call keeps them
+    int64_t z_ld;
     // kDz
     RowStats stats;
     int32_t col0;         // first column of the piece
@@ -249,6 +253,13 @@ __device__ __forceinline__ void rows_loss(const GemmArgs& g, int part, int col0,
 {
     const int hit = hit_at(g, me.target, col0, width);
     const int cols = min(width, g.v - col0);
+    if (g.z && row < g.n) {
+        float* to = g.z + (int64_t)row * g.z_ld + col0;
+#pragma unroll
+        for (int k = 0; k < kHalf; k += 8)
+            if (k < width)
+                store32(to + k, z + k);
+    }
     if (cols < kHalf) {
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
@@ -887,6 +898,8 @@ xent_few_kernel(const __grid_constant__ GemmArgs g, const uint16_t* hidden, int6
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             const float z = sum_rows(acc[0][n], acc[1][n], acc[2][n], acc[3][n], lane);
+            if (g.z && n < g.n && u < g.v && (lane & 7) == 0)
+                g.z[n * g.z_ld + u] = z;
             if (u < g.v && u != target[n])
                 add_part(m[n], s[n], z, 1.0f);
         }
@@ -1098,6 +1111,52 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
     }
 }
 
+// dz from kept logits, as rows_dz makes it: eight columns of four rows to a
+// thread, the columns that were multiplied last (and are in L2) first.
+constexpr int kDzRows = 4, kDzCols = 8 * 256;
+
+template <bool kBf16>
+__global__ void __launch_bounds__(256) xent_dz_kernel(const __grid_constant__ GemmArgs g, uint16_t* dz, int64_t dz_ld)
+{
+    let_next_start();
+    wait_for_previous();
+    const int groups = (g.n + kDzRows - 1) / kDzRows, chunks = (g.v + kDzCols - 1) / kDzCols;
+    for (int64_t i = blockIdx.x; i < (int64_t)groups * chunks; i += gridDim.x) {
+        const int chunk = chunks - 1 - (int)(i / groups), row0 = (int)(i % groups) * kDzRows;
+        const int col = chunk * kDzCols + threadIdx.x * 8;
+        if (col >= g.v)
+            continue;
+        float z[kDzRows][8];
+        Row me[kDzRows];
+#pragma unroll
+        for (int q = 0; q < kDzRows; ++q) {
+            const int row = min(row0 + q, g.n - 1);
+            load32(g.z + (int64_t)row * g.z_ld + col, z[q]);
+            me[q] = row_at<kDz>(g, row);
+        }
+#pragma unroll
+        for (int q = 0; q < kDzRows; ++q) {
+            if (row0 + q >= g.n)
+                break;
+            const bool live = me[q].target != g.ignore;
+            const float base = fmaf(-me[q].lse, kLog2e, g.exponent);
+            const int hit = hit_at(g, me[q].target, col, 8);
+            float e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                e[k] = live && col + k < g.v ? exp2_fast(fmaf(z[q][k], kLog2e, base)) : 0.0f;
+            if (hit >= 0) {
+                const float at_target = ldexpf(expm1f(-me[q].loss), (int)g.exponent);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    e[k] = k == hit ? at_target : e[k];
+            }
+            *reinterpret_cast<uint4*>(dz + (int64_t)(row0 + q) * dz_ld + col) =
+                make_uint4(pack2<kBf16>(e[0], e[1]), pack2<kBf16>(e[2], e[3]), pack2<kBf16>(e[4], e[5]), pack2<kBf16>(e[6], e[7]));
+        }
+    }
+}
+
 // dH = T(g * the sum of the splits), eight columns to a thread.
 template <bool kBf16>
 __global__ void __launch_bounds__(256)
@@ -1159,7 +1218,9 @@ struct Plan {
     int64_t piece = 0;      // columns of one piece of the backward pass
     int64_t splits = 1;     // of dH's sums over a piece
     int64_t merges = 0;
-    size_t off_part = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
+    bool keep = false;      // the logits
+    int64_t z_ld = 0;
+    size_t off_z = 0, off_part = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
            off_dh = 0, total = 0;
 };
 
@@ -1185,6 +1246,20 @@ int64_t tile_columns(int64_t mt, int64_t cols, int64_t kb, int64_t workers, int6
         }
     }
     return best;
+}
+
+// Whether it is quicker to keep a call's logits in binary32 than to multiply
+// them again.  Writing, reading and turning them into dz takes 1.4 ps each
+// (through memory); multiplying 2 d operations at 1.4 PFLOP/s, but no less than
+// reading the head at 6 TB/s, and 5 us more for a product kernel's start and
+// end.  With gradients, on the device: 77 x 1000 x 512 28 us again, 22 kept; 64 x
+// 50257 x 1024 122 and 105; 1001 x 50257 x 1024 351 and 342; the same at width
+// 512 231 and 258; 8192 x 1000 x 512 94 and 105.
+bool keeping_pays(int64_t n, int64_t v, int64_t d)
+{
+    const double logits = (double)n * (double)v;
+    const double again = 5.0 + std::max(logits * 2e-9 * (double)d / 1.4, (double)v * 2e-6 * (double)d / 6.0);
+    return logits * 1.4e-6 < again;  // us
 }
 
 int make_plan(const mpt_xent_args& a, Plan& p)
@@ -1219,6 +1294,10 @@ int make_plan(const mpt_xent_args& a, Plan& p)
         const int64_t fit = std::max<int64_t>(2048, kPieceBytes / (2 * a.n) / kTileN * kTileN);
         p.piece = std::min(round_up(a.v, kTileN), fit);
         p.off_dz = region((size_t)(a.n * p.piece * 2));
+        p.z_ld = round_up(ceil_div(a.v, p.tn_loss) * p.tn_loss, 64);
+        p.keep = a.n * p.z_ld * 4 <= kPieceBytes && keeping_pays(a.n, a.v, a.d);
+        if (p.keep)
+            p.off_z = region((size_t)(a.n * p.z_ld * 4));
         p.tn_dz = tile_columns(ceil_div(a.n, rows), p.piece, ceil_div(a.d, kTileK), workers, 128);
         // few gradient tiles: narrower ones, so that more CTAs have one
         const int64_t tiles = (p.want_dh ? ceil_div(a.n, rows) : 0) + (p.want_dw ? ceil_div(p.piece, rows) : 0);
@@ -1354,6 +1433,7 @@ bool load_kernels()
            allow_smem(xent_few_kernel<kBf16, 1>, kFewSmem) && allow_smem(xent_few_kernel<kBf16, 2>, kFewSmem) &&
            allow_smem(xent_few_kernel<kBf16, kFew>, kFewSmem) &&
            cudaFuncGetAttributes(&fa, xent_merge_kernel<kBf16>) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, xent_dz_kernel<kBf16>) == cudaSuccess &&
            cudaFuncGetAttributes(&fa, xent_dh_kernel<kBf16>) == cudaSuccess;
 }
 
@@ -1470,6 +1550,8 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     g.part = reinterpret_cast<float2*>(ws + p.off_part);
     g.part_ld = (int32_t)p.parts;
     g.control = control;
+    g.z = p.keep ? reinterpret_cast<float*>(ws + p.off_z) : nullptr;
+    g.z_ld = p.z_ld;
     g.stats = {lse, token};
     g.exponent = kBf16 ? 0.0f : 15.0f;
     g.poison = a.loss;
@@ -1519,7 +1601,7 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     uint16_t* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
     auto wide = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
     float* dh = reinterpret_cast<float*>(ws + p.off_dh);
-    if (p.few && !make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows))
+    if (p.few && !p.keep && !make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows))
         return MPT_ERR_CUDA;
     GemmArgs z = g;
     GemmArgs q = g;
@@ -1528,13 +1610,19 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     for (int64_t c0 = 0; c0 < a.v; c0 += p.piece) {
         const int64_t cols = std::min(p.piece, a.v - c0);
         const uint16_t* wp = w + c0 * a.ld_weight;
-        z.col0 = (int32_t)c0;
-        set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band, p.tn_dz);
-        if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, (int)p.tn_dz / (pair ? 2 : 1)) ||
-            !make_map(&z.out[0], kBf16, dz, a.n, cols, p.piece, kRows))
-            return MPT_ERR_CUDA;
-        if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
-            return MPT_ERR_CUDA;
+        if (p.keep) {  // one piece
+            const int64_t items = ceil_div(a.n, kDzRows) * ceil_div(a.v, kDzCols);
+            if (launch_next(xent_dz_kernel<kBf16>, std::min<int64_t>(items, kMaxCtas * 8), 256, st, g, dz, p.piece) != cudaSuccess)
+                return MPT_ERR_CUDA;
+        } else {
+            z.col0 = (int32_t)c0;
+            set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band, p.tn_dz);
+            if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, (int)p.tn_dz / (pair ? 2 : 1)) ||
+                !make_map(&z.out[0], kBf16, dz, a.n, cols, p.piece, kRows))
+                return MPT_ERR_CUDA;
+            if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
+                return MPT_ERR_CUDA;
+        }
 
         q.job[0] = q.job[1] = Job{};
         // the job of the longer tiles comes first

@@ -86,6 +86,8 @@ def test_workspace_bytes():
     logits = 8192 * 50257 * 2
     assert ws(**big, **none) < logits // 20                # row statistics
     assert ws(**big) < logits                               # a piece of dz and sums of dH
+    # never more than a piece of kept logits (256 MB) and dz (half of it)
+    assert ws(n=1300, v=50257, d=1024, ld_hidden=1024, ld_weight=1024, grad_hidden=None) < 420 << 20
     assert ws(**big, **none) < ws(**big)
     assert ws(n=0) < 4096
     nb = ctypes.c_size_t()
@@ -311,6 +313,25 @@ def test_extreme_logits(n):
     h[1, 5] = math.nan
     r = lsf.xent_loss(h, w, t)
     assert math.isnan(r.token_loss[1].item()) and int(torch.isnan(r.token_loss).sum()) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["float16", "bfloat16"])
+@pytest.mark.parametrize("shape", [(128, 50257, 64), (100, 60001, 72), (2500, 3001, 72), (6000, 1000, 136),
+                                   (1100, 8111, 264), (700, 20000, 512)], ids=lambda s: "x".join(map(str, s)))
+def test_logits_multiplied_again_in_one_piece(shape, kind):
+    """Many logits of narrow rows: quicker to multiply again than to keep."""
+    n, v, d = shape
+    h, w, t = _inputs(n, v, d, kind, 20)
+    scale = 16.0 * n if kind == "float16" else 1.0
+    _check(lsf.xent_grad(h, w, t, scale=scale), _reference(h, w, t, scale))
+
+
+@pytest.mark.gpu
+def test_few_rows_of_the_largest_vocabulary():
+    """2^24 classes: too many logits to keep, even of four rows."""
+    h, w, t = _inputs(4, 1 << 24, 8, "bfloat16", 21, ignored=0.0)
+    _check(lsf.xent_grad(h, w, t), _reference(h, w, t, 1.0))
 
 
 @pytest.mark.gpu
