@@ -1482,14 +1482,19 @@ cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
     lc.dynamicSmemBytes = S::kSmem;
     lc.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S::kCtas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    int attrs = 0;
+    if (kPair) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = S::kCtas;
+        attr[attrs].val.clusterDim.y = 1;
+        attr[attrs++].val.clusterDim.z = 1;
+    }
+    if (kMode != kLoss) {  // the first of the chain follows others' work
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     lc.attrs = attr;
-    lc.numAttrs = kMode == kLoss ? 1 : 2;  // the first of the chain follows others' work
+    lc.numAttrs = attrs;
     return cudaLaunchKernelEx(&lc, xent_product_kernel<kPair, kMode, kBf16>, g);
 }
 
