@@ -21,7 +21,7 @@
 // precision; the loss scale and 1/n are applied to the binary32 sums.
 //
 // All four products run on the tensor cores in one kernel: one CTA per SM,
-// one thread that loads tiles by TMA, one that issues the products, eight
+// one warp that loads tiles by TMA, one that issues the products, eight
 // warps that turn finished accumulators into results; two accumulators in
 // tensor memory let the products of a tile run under the results of the last.
 // Two CTAs share a tile of 256 x 256 (each loads half of either operand, so
@@ -215,7 +215,7 @@ __device__ __forceinline__ bool next_tile(const GemmArgs& g, int worker, int wor
 }
 
 // ---------------------------------------------------------------------------
-// results: one thread per row of the tile, 32 columns at a time
+// results: one thread per row and half of the tile's columns
 // ---------------------------------------------------------------------------
 
 // What a result thread has to know of its row; read before the accumulator is
@@ -242,8 +242,10 @@ __device__ __forceinline__ Row row_at(const GemmArgs& g, int row)
 // The target's column among `width` ones from col0 on, or -1.
 __device__ __forceinline__ int hit_at(const GemmArgs& g, int64_t target, int col0, int width)
 {
-    const int64_t h = target - col0;
-    return target >= 0 && target < g.v && target != g.ignore && h >= 0 && h < width ? (int)h : -1;
+    if (target < 0 || target >= g.v || target == g.ignore)
+        return -1;
+    const int h = (int)target - col0;
+    return h >= 0 && h < width ? h : -1;
 }
 
 // Maximum and sum of exponentials of `width` columns; the target's column is
