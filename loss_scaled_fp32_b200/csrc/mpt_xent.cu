@@ -50,10 +50,13 @@ constexpr int kResultWarps = 8, kThreads = 32 * (kResultWarps + 2);  // then one
 constexpr int kBytesA = kRows * kTileK * 2;
 constexpr int kHalf = kTileN / 2;       // columns of one result warp
 // The tensor cores drop what lies below an accumulator's last place, 16 of K
-// at a time, which adds up in large logits: the losses of 509 x 50257 x 2048
-// were 2e-6 off.  The forward pass therefore takes its sums out after 512 of K
-// and adds them with rounding to nearest (1e-7, with the target's logit formed
-// apart); the backward pass, whose results are rounded to 16 bits, need not.
+// at a time: 1e-7 of the sum each time where the terms have one sign, always
+// downwards.  Logits are therefore taken out after 512 of K and added with
+// rounding to nearest (losses of 509 x 50257 x 2048 2e-6 off without, 1e-7
+// with, the target's logit formed apart), in the backward pass as in the
+// forward pass: a logit that is multiplied again has to be the one that its
+// row's sum of exponentials was made from.  (Logits of 1000 to 2000, 4096 and
+// 8192 wide, gave gradients 10% and 38% off where the backward pass did not.)
 constexpr int kPromote = 512 / kTileK;
 
 // Results leave through shared memory: each half of the result warps has one
@@ -325,8 +328,8 @@ struct Box {
 
 // dz of 128 columns, rounded to 16 bits once.
 template <bool kBf16>
-__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, int row0, const Row& me, uint32_t tmem,
-                                        const Box& box)
+__device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, int row0, const Row& me,
+                                        float (&z)[kHalf], const Box& box)
 {
     const int cols = min(width, g.v - g.col0 - col0);  // col0 counts inside the piece
     const int hit = hit_at(g, me.target, g.col0 + col0, width);
@@ -334,40 +337,32 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, 
     const bool edge = cols < width || !__all_sync(0xffffffffu, live);
     const float base = fmaf(-me.lse, kLog2e, g.exponent);
     const uint64_t scale2 = pair_of(kLog2e, kLog2e), base2 = pair_of(base, base);
-#pragma unroll 1
-    for (int c = 0; c < width; c += 64) {
-        __syncwarp();
-        uint32_t r[2][32];
-        tmem_load32(tmem + c, r[0]);
-        tmem_load32(tmem + c + 32, r[1]);
-        tmem_wait_load(r[0]);
-        tmem_wait_load(r[1]);
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 64) {
+        if (c >= width)
+            break;
         const bool hits = __any_sync(0xffffffffu, hit >= c && hit < c + 64);
+#pragma unroll
+        for (int k = c; k < c + 64; k += 2) {
+            const float2 e = of_pair(fma2(pair_of(z[k], z[k + 1]), scale2, base2));
+            z[k] = exp2_fast(e.x);
+            z[k + 1] = exp2_fast(e.y);
+        }
+        if (edge) {
+#pragma unroll
+            for (int k = c; k < c + 64; ++k)
+                z[k] = live && k < cols ? z[k] : 0.0f;
+        }
+        if (hits) {
+            const float at_target = ldexpf(expm1f(-me.loss), (int)g.exponent);
+#pragma unroll
+            for (int k = c; k < c + 64; ++k)
+                z[k] = k == hit ? at_target : z[k];
+        }
         uint32_t o[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            float* z = reinterpret_cast<float*>(r[q]);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-                const float2 e = of_pair(fma2(pair_of(z[k], z[k + 1]), scale2, base2));
-                z[k] = exp2_fast(e.x);
-                z[k + 1] = exp2_fast(e.y);
-            }
-            if (edge) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    z[k] = live && c + 32 * q + k < cols ? z[k] : 0.0f;
-            }
-            if (hits) {
-                const float at_target = ldexpf(expm1f(-me.loss), (int)g.exponent);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    z[k] = c + 32 * q + k == hit ? at_target : z[k];
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                o[16 * q + k] = pack2<kBf16>(z[2 * k], z[2 * k + 1]);
-        }
+        for (int k = 0; k < 32; ++k)
+            o[k] = pack2<kBf16>(z[c + 2 * k], z[c + 2 * k + 1]);
         box.open();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -625,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                         break;
                     fence_after_sync();
                     const uint32_t d = tmem + buf * kTileN;
-                    const int last = kMode == kLoss ? min(u.kb1 - kb, kPromote) + kb : u.kb1;
+                    const int last = kMode != kGrad ? min(u.kb1 - kb, kPromote) + kb : u.kb1;
                     uint32_t add = 0;
                     // whether the next step's tiles are there is asked before
                     // this step's products are issued
@@ -703,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             const int row0 = u.m * S::kTileM + (int)rank * kRows;
             const int width = u.tn / 2, col0 = u.n * u.tn + half * width;
             const Row me = row_at<kMode>(g, row0 + quad * 32 + lane);
-            if constexpr (kMode == kLoss) {
+            if constexpr (kMode != kGrad) {
                 float z[kHalf];
                 for (int kb = u.kb0; ok && kb < u.kb1; kb += kPromote) {
                     if (!await())
@@ -734,15 +729,17 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     }
                     give_back();
                 }
-                if (ok)
-                    rows_loss(g, 2 * u.n + half, col0, width, row0 + quad * 32 + lane, me, z);
+                if (ok) {
+                    if constexpr (kMode == kLoss)
+                        rows_loss(g, 2 * u.n + half, col0, width, row0 + quad * 32 + lane, me, z);
+                    else
+                        rows_dz<kBf16>(g, col0, width, row0, me, z, box);
+                }
             } else {
                 if (!await())
                     break;
                 const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
-                if constexpr (kMode == kDz)
-                    rows_dz<kBf16>(g, col0, width, row0, me, at, box);
-                else if (!g.job[u.job].final)
+                if (!g.job[u.job].final)
                     rows_dh(g, &g.out[u.job], u.split, col0, width, row0, at, box);
                 else
                     rows_final<kBf16>(g, g.job[u.job], &g.out[u.job], col0, width, row0, at, box);

@@ -328,6 +328,36 @@ def test_logits_multiplied_again_in_one_piece(shape, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["float16", "bfloat16"])
+def test_logits_multiplied_again_are_those_of_the_loss(kind):
+    """Logits of about 2000, all of one sign: what the tensor cores drop adds up
+    in each, and only cancels against the row's lse where the backward pass
+    makes the same logits again.  Rows of a large call (multiplied again)
+    against the same rows of a small one (logits kept).  Both round the same
+    dz but for the places of lse (2 steps of 2^-23) and for what that moves
+    across a rounding to 16 bits (2 u); their sums over v differ in order, and
+    each result is rounded once."""
+    import torch
+    n, v, d, few = 4200, 16400, 8192, 200
+    g = torch.Generator(device="cuda").manual_seed(22)
+    dt = getattr(torch, kind)
+    h = (1 + 0.01 * torch.randn(n, d, generator=g, device="cuda")).to(dt)
+    w = (0.25 + 0.01 * torch.randn(v, d, generator=g, device="cuda")).to(dt)
+    t = torch.randint(0, v, (n,), generator=g, device="cuda")
+    again = lsf.xent_grad(h, w, t, scale=64.0, reduction="sum", grad_weight=None)
+    kept = lsf.xent_grad(h[:few], w, t[:few], scale=64.0, reduction="sum")
+    W = w.double()
+    z = h[:few].double() @ W.t()
+    p = 64.0 * torch.softmax(z, 1)
+    size = p @ W.abs() + 64.0 * W[t[:few]].abs()
+    assert float(z.min()) > 1900.0
+    u = torch.finfo(dt).eps / 2
+    tol = size * (2 * u + float(kept.lse.max()) * 2.0 ** -22 + 2 * (v / 16 + 64) * 2.0 ** -23) + \
+        2 * u * kept.grad_hidden.double().abs() + 2.0 ** -24
+    _close(again.grad_hidden[:few], kept.grad_hidden.double(), tol, "grad_hidden")
+
+
+@pytest.mark.gpu
 def test_few_rows_of_the_largest_vocabulary():
     """2^24 classes: too many logits to keep, even of four rows."""
     h, w, t = _inputs(4, 1 << 24, 8, "bfloat16", 21, ignored=0.0)
