@@ -1042,11 +1042,13 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
         float total = others;
         if (valid) {
             if (known) {
-                const float over = others - zt;
-                loss = fmaxf(over, 0.0f) + log1pf(expf(-fabsf(over)));
+                // lse from the larger of the two: with the target far below the
+                // others zt + loss would keep the places of zt, and be NaN at -inf
+                const float over = others - zt, small = log1pf(expf(-fabsf(over)));
+                loss = fmaxf(over, 0.0f) + small;
                 if (isnan(over))
                     loss = over;  // fmaxf drops a NaN
-                total = zt + loss;
+                total = over > 0.0f ? others + small : zt + loss;
             } else {
                 loss = total = __int_as_float(0x7fc00000);  // no such class
             }

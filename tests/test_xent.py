@@ -316,6 +316,60 @@ def test_extreme_logits(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 600, 64), (90, 600, 64), (300, 600, 64), (6000, 1000, 136)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("low", [-math.inf, -3e4])
+def test_a_target_far_below_the_others(low, shape):
+    """lse keeps its places, and a target's logit of -inf leaves the row an
+    infinite loss and finite probabilities.  (Logits kept and multiplied again;
+    the column of the low logit is left out of A and of the largest |z|: its
+    products are 0 but for one, which is exact.)"""
+    import torch
+    n, v, d = shape
+    h, w, t = _inputs(n, v, d, "float16", 23, ignored=0.0, std=0.3)
+    h[:, 0] = 1.0
+    w[:, 0] = 0.0
+    w[7] = 0.0
+    w[7, 0] = low
+    t[t == 7] = 8
+    t[n // 2] = 7
+    keep = torch.arange(v, device="cuda") != 7
+    # without class 7, whose probability is 0 (the row's target: any other)
+    t0 = torch.where(t == 7, 0, t - (t > 7).long())
+    ref = _reference(h, w[keep], t0, 16.0 * n)
+    e = ref["e"]
+    r = lsf.xent_grad(h, w, t, scale=16.0 * n, grad_hidden=True)
+    _close(r.lse, ref["lse"], e + ref["lse"].abs() * 2.0 ** -23, "lse")
+    row = n // 2
+    if low == -math.inf:
+        assert r.token_loss[row].item() == math.inf and r.loss.item() == math.inf
+    else:
+        want = ref["lse"][row] - low
+        _close(r.token_loss[row], want, 2 * e + want * 2.0 ** -23, "token_loss")
+    # dW: the row adds p h to the others (its stand-in class 0 took h away) and
+    # -h to class 7
+    H = h.double()
+    dw = torch.zeros(v, d, dtype=torch.float64, device="cuda")
+    dw[keep] = ref["dw"]
+    dw[0] += 16.0 * H[row]
+    dw[7] = -16.0 * H[row]
+    tol = torch.zeros_like(dw)
+    tol[keep] = ref["tol_dw"]
+    tol[7] = 16.0 * H[row].abs() * 2.0 ** -9
+    tol[0] += 16.0 * H[row].abs() * 2.0 ** -9
+    _close(r.grad_weight, dw, tol, "grad_weight")
+    # dH of the other rows; of this one beside the column of the low weight,
+    # where the other classes' sum is 0 and this class adds -(low)
+    others = torch.arange(n, device="cuda") != row
+    _close(r.grad_hidden[others][:, 1:], ref["dh"][others][:, 1:], ref["tol_dh"][others][:, 1:], "grad_hidden")
+    if low != -math.inf:
+        W = w.double()
+        dh = ref["dh"][row] + 16.0 * W[0]
+        assert bool(((r.grad_hidden[row].double() - dh)[1:].abs() <=
+                     (ref["tol_dh"][row] + 16.0 * W[0].abs() * 2.0 ** -9)[1:]).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["float16", "bfloat16"])
 @pytest.mark.parametrize("shape", [(128, 50257, 64), (100, 60001, 72), (2500, 3001, 72), (6000, 1000, 136),
                                    (1100, 8111, 264), (700, 20000, 512)], ids=lambda s: "x".join(map(str, s)))
