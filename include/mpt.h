@@ -492,7 +492,10 @@ int mpt_list_destroy(mpt_list* h);
  * and S/n is applied in binary32 before the gradients are rounded: a value
  * beyond FP16's range becomes inf there, which mpt_step finds and skips on.
  * A target that is neither ignored nor a class makes the loss and the
- * gradients NaN (and nothing out of range is read).  Each result depends on
+ * gradients NaN (and nothing out of range is read), and so does a logit of
+ * +inf or NaN, as an overflow in the layers below leaves it; one of -inf is a
+ * class of probability 0 (as target: a loss of +inf).  Rows that are ignored
+ * have to be finite, too: grad_weight adds 0 times them.  Each result depends on
  * the call's arguments alone, bit for bit: no sum's order depends on timing. */
 #define MPT_XENT_MEAN 0
 #define MPT_XENT_SUM 1

@@ -1046,9 +1046,9 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
                 // others zt + loss would keep the places of zt, and be NaN at -inf
                 const float over = others - zt, small = log1pf(expf(-fabsf(over)));
                 loss = fmaxf(over, 0.0f) + small;
-                if (isnan(over))
-                    loss = over;  // fmaxf drops a NaN
                 total = over > 0.0f ? others + small : zt + loss;
+                if (isnan(over) || zt == INFINITY)  // (fmaxf drops a NaN)
+                    loss = total = __int_as_float(0x7fc00000);
             } else {
                 loss = total = __int_as_float(0x7fc00000);  // no such class
             }

@@ -370,6 +370,29 @@ def test_a_target_far_below_the_others(low, shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 90, 300])
+def test_a_logit_of_plus_infinity_is_never_sure(n):
+    """log(sum exp z) - z_t is inf - inf where the target's logit is +inf: NaN,
+    not a loss of 0 that would hide the overflow."""
+    import torch
+    h, w, t = _inputs(n, 600, 64, "float16", 24, ignored=0.0)
+    w[:, 0] = 0.0
+    w[7] = 0.0
+    w[7, 0] = math.inf
+    h[:, 0] = -1.0                                # -inf for the other rows
+    h[n // 2, 0] = 1.0
+    t[t == 7] = 8
+    for target in (7, 8):
+        t[n // 2] = target
+        r = lsf.xent_grad(h, w, t)
+        for each in (r.token_loss, r.lse):
+            nan = torch.isnan(each)
+            assert nan[n // 2] and int(nan.sum()) == 1
+        assert math.isnan(r.loss.item())
+        assert bool(torch.isnan(r.grad_hidden[n // 2]).all()) and bool(torch.isnan(r.grad_weight).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["float16", "bfloat16"])
 @pytest.mark.parametrize("shape", [(128, 50257, 64), (100, 60001, 72), (2500, 3001, 72), (6000, 1000, 136),
                                    (1100, 8111, 264), (700, 20000, 512)], ids=lambda s: "x".join(map(str, s)))
