@@ -11,8 +11,10 @@
 // multiplied; the backward pass goes through the vocabulary in pieces: multiply
 // z again, write dz of the piece in 16 bits, and multiply it with W (dH, summed
 // over the pieces in binary32) and with H (this piece's rows of dW, final at
-// once).  Where all of a call's logits fit in a piece's buffer and moving them
-// is cheaper than multiplying again, they stay there between the passes.
+// once).  More than 16384 rows are cut, too, and a piece's dW is then summed in
+// binary32 over the cuts.  Where all of a call's logits fit in a buffer of their
+// own and moving them is cheaper than multiplying again, they stay there between
+// the passes.
 //
 // The loss is formed from the other columns' sum against the target's logit,
 // so a sure answer's small loss keeps its digits, and dz at the target comes
@@ -95,6 +97,7 @@ struct Job {
     int32_t is_dw;        // kGrad: dW (else dH)
     // kGrad: results are final, g * sum in 16 bits (else binary32 sums)
     int32_t final;
+    int32_t add;          // to the sums that are there
     int32_t rows;
     int32_t wide;         // TMA can store them; if not:
     uint16_t* to;
@@ -137,7 +140,6 @@ struct GemmArgs {
     float exponent;       // dz is scaled by 2^exponent
     // kGrad
     int32_t d;
-    int32_t add;          // dH: add to what an earlier piece left there
     float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
 };
 
@@ -376,9 +378,9 @@ __device__ __forceinline__ void rows_dz(const GemmArgs& g, int col0, int width, 
     }
 }
 
-// 128 columns of dH's binary32 sums.
-__device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* out, int split, int col0, int width, int row0,
-                                        uint32_t tmem, const Box& box)
+// 128 columns of a gradient's binary32 sums.
+__device__ __forceinline__ void rows_sums(const GemmArgs& g, const Job& j, const CUtensorMap* out, int split, int col0,
+                                          int width, int row0, uint32_t tmem, const Box& box)
 {
 #pragma unroll 1
     for (int c = 0; c < width; c += 32) {
@@ -393,8 +395,8 @@ __device__ __forceinline__ void rows_dh(const GemmArgs& g, const CUtensorMap* ou
         for (int k = 0; k < 8; ++k)
             box.put(k, r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
         box.close();
-        if (box.first && row0 < g.n) {
-            if (g.add)
+        if (box.first && row0 < j.rows) {
+            if (j.add)
                 tma_store3<true>(out, box.at, col0 + c, row0, split);
             else
                 tma_store3<false>(out, box.at, col0 + c, row0, split);
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     break;
                 const uint32_t at = lanes_at + (acc & 1) * kTileN + half * width;
                 if (!g.job[u.job].final)
-                    rows_dh(g, &g.out[u.job], u.split, col0, width, row0, at, box);
+                    rows_sums(g, g.job[u.job], &g.out[u.job], u.split, col0, width, row0, at, box);
                 else
                     rows_final<kBf16>(g, g.job[u.job], &g.out[u.job], col0, width, row0, at, box);
                 give_back();
@@ -1163,10 +1165,10 @@ __global__ void __launch_bounds__(256) xent_dz_kernel(const __grid_constant__ Ge
     }
 }
 
-// dH = T(g * the sum of the splits), eight columns to a thread.
+// A gradient = T(g * the sum of the splits), eight columns to a thread.
 template <bool kBf16>
 __global__ void __launch_bounds__(256)
-xent_dh_kernel(const float* part, int32_t splits, int64_t n, int32_t d, const float* gscale, uint16_t* out,
+xent_round_kernel(const float* part, int32_t splits, int64_t n, int32_t d, const float* gscale, uint16_t* out,
                int64_t ld, int32_t wide)
 {
     wait_for_previous();
@@ -1221,17 +1223,24 @@ struct Plan {
     int64_t few_rows = 0, few_smem = 0;
     int64_t tn_loss = 0, tn_dz = 0, tn_grad = 0;  // columns of a tile
     int64_t parts = 0;      // half tiles of the whole vocabulary
+    int64_t cut = 0;        // rows that the backward pass takes at a time
     int64_t piece = 0;      // columns of one piece of the backward pass
     int64_t splits = 1;     // of dH's sums over a piece
     int64_t merges = 0;
     bool keep = false;      // the logits
     int64_t z_ld = 0;
     size_t off_z = 0, off_part = 0, off_token = 0, off_lse = 0, off_merge = 0, off_ctl = 0, off_dz = 0,
-           off_dh = 0, total = 0;
+           off_dh = 0, off_dw = 0, total = 0;
 };
 
-// The piece: dz of one piece is at most 256 MB (and at least 2048 columns).
+// The piece: dz of one piece (of a cut's rows) is at most 256 MB.
 constexpr int64_t kPieceBytes = 256ll << 20;
+// The longest sum that stays in tensor memory, in blocks of 64.  What the tensor
+// cores drop comes to 6.5e-9 of a sum of one sign for each of K: 1.1e-4 of 16384,
+// a fifth of binary16's half step.  (dW of 131072 rows in one sum was 8e-4 off,
+// of 1048576 rows 7e-3.)  Longer ones are cut, dH's in splits, dW's by its rows,
+// and the parts are added with rounding to nearest.
+constexpr int64_t kLongestSum = 256;
 constexpr int64_t kLeastSplit = 16;  // blocks of 64 in one part of a cut sum
 
 // Columns of a tile: as many as 256, unless narrower tiles, which are a
@@ -1297,24 +1306,28 @@ int make_plan(const mpt_xent_args& a, Plan& p)
     p.off_lse = region(sizeof(float) * (size_t)a.n);
     p.off_merge = region(sizeof(MergePart) * (size_t)p.merges);
     if (p.grad && a.n > 0) {
-        const int64_t fit = std::max<int64_t>(2048, kPieceBytes / (2 * a.n) / kTileN * kTileN);
-        p.piece = std::min(round_up(a.v, kTileN), fit);
-        p.off_dz = region((size_t)(a.n * p.piece * 2));
+        p.cut = round_up(ceil_div(a.n, ceil_div(a.n, kLongestSum * kTileK)), 2 * kRows);
+        p.cut = std::min(p.cut, a.n);
+        p.piece = std::min(round_up(a.v, kTileN), kPieceBytes / (2 * p.cut) / kTileN * kTileN);
+        p.off_dz = region((size_t)(p.cut * p.piece * 2));
         p.z_ld = round_up(ceil_div(a.v, p.tn_loss) * p.tn_loss, 64);
-        p.keep = a.n * p.z_ld * 4 <= kPieceBytes && keeping_pays(a.n, a.v, a.d);
+        p.keep = a.n * p.z_ld * 4 <= kPieceBytes && p.piece >= a.v && keeping_pays(a.n, a.v, a.d);
         if (p.keep)
             p.off_z = region((size_t)(a.n * p.z_ld * 4));
-        p.tn_dz = tile_columns(ceil_div(a.n, rows), p.piece, ceil_div(a.d, kTileK), workers, 128);
+        p.tn_dz = tile_columns(ceil_div(p.cut, rows), p.piece, ceil_div(a.d, kTileK), workers, 128);
         // few gradient tiles: narrower ones, so that more CTAs have one
-        const int64_t tiles = (p.want_dh ? ceil_div(a.n, rows) : 0) + (p.want_dw ? ceil_div(p.piece, rows) : 0);
+        const int64_t tiles = (p.want_dh ? ceil_div(p.cut, rows) : 0) + (p.want_dw ? ceil_div(p.piece, rows) : 0);
         p.tn_grad = 2 * tiles * ceil_div(a.d, kTileN) <= workers ? 128 : 256;
+        if (p.want_dw && p.cut < a.n)
+            p.off_dw = region((size_t)(p.piece * a.d * 4));
         if (p.want_dh) {
             // cut dH's sums so that one tile is at most half a CTA's share of the piece's work
-            const int64_t kb_v = ceil_div(p.piece, kTileK), kb_n = ceil_div(a.n, kTileK);
-            const int64_t tiles_h = ceil_div(a.n, kRows) * ceil_div(a.d, kTileN);
+            const int64_t kb_v = ceil_div(p.piece, kTileK), kb_n = ceil_div(p.cut, kTileK);
+            const int64_t tiles_h = ceil_div(p.cut, kRows) * ceil_div(a.d, kTileN);
             const int64_t tiles_w = p.want_dw ? ceil_div(p.piece, kRows) * ceil_div(a.d, kTileN) : 0;
             const int64_t share = (tiles_h * kb_v + tiles_w * kb_n) / kMaxCtas;
             p.splits = std::min<int64_t>(64, ceil_div(kb_v, std::max<int64_t>(kLeastSplit, share / 2)));
+            p.splits = std::max(p.splits, ceil_div(kb_v, kLongestSum));
             p.dh_final = p.splits == 1 && p.piece >= a.v;
             if (!p.dh_final)
                 p.off_dh = region((size_t)(p.splits * a.n * a.d * 4));
@@ -1393,17 +1406,17 @@ EncodeFn encode_fn()
     return reinterpret_cast<EncodeFn>(f);
 }
 
-// [planes] of a row-major matrix, cut into boxes of 128 bytes by box_rows; what
-// lies outside reads as zero and is not written.
-bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t planes, int64_t rows, int64_t cols,
-              int64_t ld, int box_rows)
+// [planes], `plane` elements apart, of a row-major matrix, cut into boxes of 128
+// bytes by box_rows; what lies outside reads as zero and is not written.
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t planes, int64_t plane, int64_t rows,
+              int64_t cols, int64_t ld, int box_rows)
 {
     EncodeFn f = encode_fn();
     if (!f)
         return false;
     const int64_t width = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)(ld * width), (cuuint64_t)(rows * ld * width)};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * width), (cuuint64_t)(plane * width)};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / width), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     return f(m, type, planes ? 3 : 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1413,8 +1426,8 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* p, int64_t p
 
 bool make_map(CUtensorMap* m, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows)
 {
-    return make_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 0, rows, cols, ld,
-                    box_rows);
+    return make_map(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 0, 0, rows, cols,
+                    ld, box_rows);
 }
 
 template <class K>
@@ -1440,7 +1453,7 @@ bool load_kernels()
            allow_smem(xent_few_kernel<kBf16, kFew>, kFewSmem) &&
            cudaFuncGetAttributes(&fa, xent_merge_kernel<kBf16>) == cudaSuccess &&
            cudaFuncGetAttributes(&fa, xent_dz_kernel<kBf16>) == cudaSuccess &&
-           cudaFuncGetAttributes(&fa, xent_dh_kernel<kBf16>) == cudaSuccess;
+           cudaFuncGetAttributes(&fa, xent_round_kernel<kBf16>) == cudaSuccess;
 }
 
 // Once per device, at its first call: every kernel is loaded and may use its
@@ -1612,72 +1625,91 @@ int enqueue(const mpt_xent_args& a, const Plan& p, char* ws, cudaStream_t st)
     uint16_t* dz = reinterpret_cast<uint16_t*>(ws + p.off_dz);
     auto wide = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
     float* dh = reinterpret_cast<float*>(ws + p.off_dh);
-    if (p.few && !p.keep && !make_map(&g.a[0], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kRows))
-        return MPT_ERR_CUDA;
-    GemmArgs z = g;
-    GemmArgs q = g;
+    float* dw = reinterpret_cast<float*>(ws + p.off_dw);
+    // T(gscale * the sum of `parts` planes of rows x d)
+    auto round_sums = [&](const float* sums, int32_t parts, int64_t rows, uint16_t* to, int64_t ld) {
+        const int64_t blocks = std::min<int64_t>(ceil_div(rows * (a.d / 8), 256), 148 * 8);
+        return launch_next(xent_round_kernel<kBf16>, blocks, 256, st, sums, parts, rows, (int32_t)a.d,
+                           (const float*)&control->gscale, to, ld, (int32_t)wide(to, ld)) == cudaSuccess;
+    };
     const uint16_t* w = static_cast<const uint16_t*>(a.weight);
+    uint16_t* grad_w = static_cast<uint16_t*>(a.grad_weight);
     const int32_t splits = p.want_dh ? (int32_t)std::min(p.splits, ceil_div(std::min(p.piece, a.v), kTileK)) : 0;
+    const bool dw_final = p.cut >= a.n;
     for (int64_t c0 = 0; c0 < a.v; c0 += p.piece) {
         const int64_t cols = std::min(p.piece, a.v - c0);
         const uint16_t* wp = w + c0 * a.ld_weight;
-        if (p.keep) {  // one piece
-            const int64_t items = ceil_div(a.n, kDzRows) * ceil_div(a.v, kDzCols);
-            if (launch_next(xent_dz_kernel<kBf16>, std::min<int64_t>(items, kMaxCtas * 8), 256, st, g, dz, p.piece) != cudaSuccess)
-                return MPT_ERR_CUDA;
-        } else {
+        for (int64_t r0 = 0; r0 < a.n; r0 += p.cut) {
+            const int64_t rows = std::min(p.cut, a.n - r0);
+            const uint16_t* hp = m.hidden + r0 * a.ld_hidden;
+            GemmArgs z = g;
+            z.n = (int32_t)rows;
+            z.targets = static_cast<const char*>(a.targets) + r0 * a.target_bytes;
+            z.stats = {lse + r0, token + r0};
             z.col0 = (int32_t)c0;
-            set_job(z.job[0], pair, kBf16, a.n, cols, a.d, 1, false, false, band, p.tn_dz);
-            if (!make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, (int)p.tn_dz / (pair ? 2 : 1)) ||
-                !make_map(&z.out[0], kBf16, dz, a.n, cols, p.piece, kRows))
-                return MPT_ERR_CUDA;
-            if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
-                return MPT_ERR_CUDA;
-        }
+            z.job[0] = z.job[1] = Job{};
+            GemmArgs q = z;
+            if (p.keep) {  // one piece
+                z.z = g.z + r0 * p.z_ld;
+                const int64_t items = ceil_div(rows, kDzRows) * ceil_div(a.v, kDzCols);
+                if (launch_next(xent_dz_kernel<kBf16>, std::min<int64_t>(items, kMaxCtas * 8), 256, st, z, dz, p.piece) != cudaSuccess)
+                    return MPT_ERR_CUDA;
+            } else {
+                set_job(z.job[0], pair, kBf16, rows, cols, a.d, 1, false, false, band, p.tn_dz);
+                if (!make_map(&z.a[0], kBf16, hp, rows, a.d, a.ld_hidden, kRows) ||
+                    !make_map(&z.b[0], kBf16, wp, cols, a.d, a.ld_weight, (int)p.tn_dz / (pair ? 2 : 1)) ||
+                    !make_map(&z.out[0], kBf16, dz, rows, cols, p.piece, kRows))
+                    return MPT_ERR_CUDA;
+                if (launch_product<kDz, kBf16>(pair, z, st) != cudaSuccess)
+                    return MPT_ERR_CUDA;
+            }
 
-        q.job[0] = q.job[1] = Job{};
-        // the job of the longer tiles comes first
-        const int64_t kb_h = p.want_dh ? ceil_div(ceil_div(cols, kTileK), splits) : 0;
-        const int at_h = kb_h >= ceil_div(a.n, kTileK) || !p.want_dw ? 0 : 1, at_w = p.want_dh ? 1 - at_h : 0;
-        if (p.want_dh) {
-            // (a short last piece may add to the first sums only)
-            Job& j = q.job[at_h];
-            set_job(j, pair, kBf16, a.n, a.d, cols, splits, false, true, 1, p.tn_grad);
-            q.add = c0 > 0;
-            j.final = p.dh_final;
-            j.rows = (int32_t)a.n;
-            j.wide = wide(a.grad_hidden, a.ld_grad_hidden);
-            j.to = static_cast<uint16_t*>(a.grad_hidden);
-            j.ld = a.ld_grad_hidden;
-            if (!make_map(&q.a[at_h], kBf16, dz, a.n, cols, p.piece, kRows) ||
-                !make_map(&q.b[at_h], kBf16, wp, cols, a.d, a.ld_weight, kTileK) ||
-                (!j.final && !make_map(&q.out[at_h], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dh, splits, a.n, a.d, a.d, kRows)) ||
-                (j.final && j.wide && !make_map(&q.out[at_h], kBf16, j.to, a.n, a.d, j.ld, kRows)))
+            // the job of the longer tiles comes first
+            const int64_t kb_h = p.want_dh ? ceil_div(ceil_div(cols, kTileK), splits) : 0;
+            const int at_h = kb_h >= ceil_div(rows, kTileK) || !p.want_dw ? 0 : 1, at_w = p.want_dh ? 1 - at_h : 0;
+            if (p.want_dh) {
+                // (a short last piece may add to the first sums only)
+                Job& j = q.job[at_h];
+                set_job(j, pair, kBf16, rows, a.d, cols, splits, false, true, 1, p.tn_grad);
+                j.add = c0 > 0;
+                j.final = p.dh_final;
+                j.rows = (int32_t)rows;
+                j.to = static_cast<uint16_t*>(a.grad_hidden) + r0 * a.ld_grad_hidden;
+                j.ld = a.ld_grad_hidden;
+                j.wide = wide(j.to, j.ld);
+                if (!make_map(&q.a[at_h], kBf16, dz, rows, cols, p.piece, kRows) ||
+                    !make_map(&q.b[at_h], kBf16, wp, cols, a.d, a.ld_weight, kTileK) ||
+                    (!j.final && !make_map(&q.out[at_h], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dh + r0 * a.d, splits, a.n * a.d,
+                                           rows, a.d, a.d, kRows)) ||
+                    (j.final && j.wide && !make_map(&q.out[at_h], kBf16, j.to, rows, a.d, j.ld, kRows)))
+                    return MPT_ERR_CUDA;
+            }
+            if (p.want_dw) {
+                Job& j = q.job[at_w];
+                set_job(j, pair, kBf16, cols, a.d, rows, 1, true, true, 1, p.tn_grad);
+                j.is_dw = 1;
+                j.final = dw_final;
+                j.add = r0 > 0;
+                j.rows = (int32_t)cols;
+                j.to = grad_w + c0 * a.ld_grad_weight;
+                j.ld = a.ld_grad_weight;
+                j.wide = wide(j.to, j.ld);
+                if (!make_map(&q.a[at_w], kBf16, dz, rows, cols, p.piece, kTileK) ||
+                    !make_map(&q.b[at_w], kBf16, hp, rows, a.d, a.ld_hidden, kTileK) ||
+                    (!j.final && !make_map(&q.out[at_w], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dw, 1, cols * a.d, cols, a.d, a.d,
+                                           kRows)) ||
+                    (j.final && j.wide && !make_map(&q.out[at_w], kBf16, j.to, cols, a.d, j.ld, kRows)))
+                    return MPT_ERR_CUDA;
+            }
+            if (launch_product<kGrad, kBf16>(pair, q, st) != cudaSuccess)
                 return MPT_ERR_CUDA;
         }
-        if (p.want_dw) {
-            Job& j = q.job[at_w];
-            set_job(j, pair, kBf16, cols, a.d, a.n, 1, true, true, 1, p.tn_grad);
-            j.is_dw = j.final = 1;
-            j.rows = (int32_t)cols;
-            j.wide = wide(a.grad_weight, a.ld_grad_weight);
-            j.to = static_cast<uint16_t*>(a.grad_weight) + c0 * a.ld_grad_weight;
-            j.ld = a.ld_grad_weight;
-            if (!make_map(&q.a[at_w], kBf16, dz, a.n, cols, p.piece, kTileK) ||
-                !make_map(&q.b[at_w], kBf16, a.hidden, a.n, a.d, a.ld_hidden, kTileK) ||
-                (j.wide && !make_map(&q.out[at_w], kBf16, j.to, cols, a.d, j.ld, kRows)))
-                return MPT_ERR_CUDA;
-        }
-        if (launch_product<kGrad, kBf16>(pair, q, st) != cudaSuccess)
+        if (p.want_dw && !dw_final && !round_sums(dw, 1, cols, grad_w + c0 * a.ld_grad_weight, a.ld_grad_weight))
             return MPT_ERR_CUDA;
     }
-    if (p.want_dh && !p.dh_final) {
-        const int64_t blocks = std::min<int64_t>(ceil_div(a.n * (a.d / 8), 256), 148 * 8);
-        if (launch_next(xent_dh_kernel<kBf16>, blocks, 256, st, (const float*)dh, splits, a.n, (int32_t)a.d,
-                        (const float*)&control->gscale, static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden,
-                        (int32_t)wide(a.grad_hidden, a.ld_grad_hidden)) != cudaSuccess)
-            return MPT_ERR_CUDA;
-    }
+    if (p.want_dh && !p.dh_final &&
+        !round_sums(dh, splits, a.n, static_cast<uint16_t*>(a.grad_hidden), a.ld_grad_hidden))
+        return MPT_ERR_CUDA;
     return MPT_OK;
 }
 

@@ -95,6 +95,22 @@ def test_workspace_bytes():
     assert L.mpt_xent_workspace_bytes(ctypes.byref(_args(d=9)), ctypes.byref(nb)) == lsf.MPT_ERR_INVALID_ARG
 
 
+def test_workspace_of_many_rows():
+    """dz of a piece stays within 256 MB whatever the rows are (and grad_weight's
+    sums over the cuts, at most 16384 classes, beside it)."""
+    L = lsf.lib()
+
+    def ws(**kw):
+        nb = ctypes.c_size_t()
+        assert L.mpt_xent_workspace_bytes(ctypes.byref(_args(**kw)), ctypes.byref(nb)) == 0
+        return nb.value
+    for n in (9000, 20_000, 70_000, 1 << 20, 1 << 24):
+        for v in (500, 50257):
+            size = dict(n=n, v=v, d=64, ld_hidden=64, ld_weight=64, grad_hidden=None)
+            extra = ws(**size) - ws(**size, grad_weight=None)
+            assert extra <= (256 << 20) + (16384 * 64 * 4 if n > 16384 else 0) + 4096, (n, v, extra)
+
+
 # ---------------------------------------------------------------------------
 # GPU
 # ---------------------------------------------------------------------------
@@ -390,6 +406,58 @@ def test_a_logit_of_plus_infinity_is_never_sure(n):
             assert nan[n // 2] and int(nan.sum()) == 1
         assert math.isnan(r.loss.item())
         assert bool(torch.isnan(r.grad_hidden[n // 2]).all()) and bool(torch.isnan(r.grad_weight).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,kind", [(400_003, "float16"), (3_000_001, "bfloat16")])
+def test_long_sums_over_the_rows(n, kind):
+    """dW of rows that all pull one way.  Eight classes of equal logits: dz is
+    1/8 or -7/8, exact in 16 bits, so what is left is the sum: in parts of at
+    most 16384 rows, where 16 of K lose at most two of the sum's last places
+    (2 * 2^-23), the parts added to nearest, and one rounding of the result."""
+    import torch
+    dt = getattr(torch, kind)
+    g = torch.Generator(device="cuda").manual_seed(25)
+    h = (1 + torch.rand(n, 8, generator=g, device="cuda")).to(dt)
+    w = torch.zeros(8, 8, dtype=dt, device="cuda")
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    r = lsf.xent_grad(h, w, t, scale=64.0)
+    want = h.double().sum(0) * (8.0 / n) * torch.tensor([-7.0] + [1.0] * 7, dtype=torch.float64, device="cuda")[:, None]
+    rel = torch.finfo(dt).eps / 2 * 1.01 + 1024 * 2 * 2.0 ** -23 + (n / 8192) * 2.0 ** -24 + 2.0 ** -20
+    _close(r.grad_weight, want, want.abs() * rel, "grad_weight")
+    assert not r.grad_hidden.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["float16", "bfloat16"])
+@pytest.mark.parametrize("shape", [(20_000, 700, 72), (20_000, 700, 1024), (33_000, 14_000, 64), (16_641, 300, 136)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_more_rows_than_one_cut(shape, kind):
+    """Two and three cuts of the rows: logits multiplied again, logits kept,
+    and two pieces of the vocabulary; a last cut of other length."""
+    n, v, d = shape
+    h, w, t = _inputs(n, v, d, kind, 26)
+    scale = 16.0 * n if kind == "float16" else 1.0
+    ref = _reference(h, w, t, scale)
+    _check(lsf.xent_grad(h, w, t, scale=scale), ref)
+    _check(lsf.xent_grad(h, w, t, scale=scale, grad_weight=None), ref)
+    _check(lsf.xent_grad(h, w, t.int(), scale=scale, grad_hidden=None), ref)
+
+
+@pytest.mark.gpu
+def test_cuts_write_rows_with_gaps():
+    import torch
+    n, v, d = 16_400, 300, 72
+    h, w, t = _inputs(n, v, d, "float16", 27)
+    ref = _reference(h, w, t, 16.0 * n)
+    room_h = torch.full((n * 75 + 8,), 3.0, dtype=torch.float16, device="cuda")
+    room_w = torch.full((v * 73 + 8,), 3.0, dtype=torch.float16, device="cuda")
+    gh, gw = room_h[1:1 + n * 75].view(n, 75)[:, :d], room_w[3:3 + v * 73].view(v, 73)[:, :d]
+    _check(lsf.xent_grad(h, w, t, scale=16.0 * n, grad_hidden=gh, grad_weight=gw), ref)
+    for room, shift, rows, ld in ((room_h, 1, n, 75), (room_w, 3, v, 73)):
+        keep = torch.ones_like(room, dtype=torch.bool)
+        keep[shift:shift + rows * ld].view(rows, ld)[:, :d] = False
+        assert bool((room[keep] == 3.0).all())
 
 
 @pytest.mark.gpu
