@@ -544,6 +544,14 @@ int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes);
  * argument error nothing is queued. */
 int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void* cuda_stream);
 
+/* Test hook: in the next mpt_xent that this thread queues, the waits inside the
+ * named passes' product kernels give up at once where they would wait, as they
+ * do after some seconds otherwise.  Errors: MPT_ERR_INVALID_ARG. */
+#define MPT_XENT_PASS_LOSS 0x1 /* products of the loss (from five rows on)           */
+#define MPT_XENT_PASS_DZ 0x2   /* logits multiplied again (where they are not kept)  */
+#define MPT_XENT_PASS_GRAD 0x4 /* products of the gradients                          */
+int mpt_debug_xent_give_up(int32_t passes);
+
 #ifdef __cplusplus
 }
 #endif

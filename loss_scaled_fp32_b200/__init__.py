@@ -165,6 +165,7 @@ def lib():
             "mpt_xent_args_init": [ctypes.POINTER(XentArgs)],
             "mpt_xent_workspace_bytes": [ctypes.POINTER(XentArgs), ctypes.POINTER(ctypes.c_size_t)],
             "mpt_xent": [ctypes.POINTER(XentArgs), vp, ctypes.c_size_t, vp],
+            "mpt_debug_xent_give_up": [i32],
         }
         for name, args in sig.items():
             fn = getattr(L, name)

@@ -82,7 +82,7 @@ constexpr int kMaxCtas = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kAlign = 256;
 
-enum Mode { kLoss, kDz, kGrad };
+enum Mode { kLoss, kDz, kGrad };  // the places of MPT_XENT_PASS_*
 
 // One product: mt x nt output tiles, each summed over kb blocks of 64, the
 // sum cut into `splits` parts.  Tiles are taken in bands of `band` rows of
@@ -141,6 +141,7 @@ struct GemmArgs {
     // kGrad
     int32_t d;
     float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
+    int32_t give_up;      // test hook: as if a wait of every block had run out
 };
 
 __device__ __forceinline__ int64_t target_of(const GemmArgs& g, int row)
@@ -487,6 +488,30 @@ __device__ __forceinline__ void by_layout(bool dw, F&& f)
         f(Flag<true>{}, Flag<true>{});
 }
 
+// After a wait that ran out: wait (bounded) until every load that was issued has
+// landed, in either CTA of a pair; both signal the first one's barriers, which
+// alone expects their bytes.  steps0 and steps1 are the loads that the CTAs have
+// issued: no more than a ring apart, since a stage is loaded again only after
+// both its halves were multiplied.  Where one CTA is ahead the first makes up for
+// the other: it expects what only its pair has loaded, and counts what its pair
+// never will as landed.
+template <bool kPair, int kStages>
+__device__ __forceinline__ void drain_loads(uint32_t full, uint32_t steps0, uint32_t steps1, uint32_t bytes, int lane)
+{
+    const uint32_t most = max(steps0, steps1);
+    for (uint32_t b = most > kStages ? most - kStages : 0; b < most; ++b) {
+        const uint32_t bar = full + (b % kStages) * 8;
+        if (lane == 0) {
+            if (kPair && b >= steps0)
+                mbar_expect(bar, bytes);
+            if (kPair && b >= steps1)
+                mbar_landed(bar, bytes);
+        }
+        __syncwarp();
+        mbar_wait(bar, (b / kStages) & 1, nullptr);
+    }
+}
+
 template <bool kPair, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
 {
@@ -495,6 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     __shared__ alignas(8) uint64_t s_full[S::kStages], s_empty[S::kStages], s_acc_full[2], s_acc_empty[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_dead;
+    // of the CTAs that share a tile: loads issued, and whether a wait ran out
+    __shared__ uint32_t s_steps[2], s_lost[2];
 
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const uint32_t tiles_at = (smem_addr(dyn) + 1023u) & ~1023u;  // swizzle atoms are 1024 bytes
@@ -521,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             mbar_init(smem_addr(&s_acc_empty[b]), kResultWarps * S::kCtas);
         }
         mbar_init(smem_addr(&s_drain), 1);
-        s_dead = 0;
+        s_dead = g.give_up;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -599,10 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         // the last products' signals must find this block's barriers
         for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; ok && b < steps; ++b)
             ok = mbar_wait_warp(smem_addr(s_empty) + (b % S::kStages) * 8, (b / S::kStages) & 1, dead);
-        if (!ok && rank == 0) {  // let the loads in flight land before the block leaves
-            for (uint32_t b = steps > S::kStages ? steps - S::kStages : 0; b < steps; ++b)
-                mbar_wait(smem_addr(s_full) + (b % S::kStages) * 8, (b / S::kStages) & 1, nullptr);
-        }
+        if (lane == 0)
+            s_steps[rank] = steps;
     } else if (warp == kResultWarps + 1 && rank == 0) {
         // ---- products
         Ring<S::kStages> ring;
@@ -656,11 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 }
             };
             by_layout<kMode>(g.job[u.job].is_dw, run);
-        }
-        if (!ok) {  // let the products in flight end before tensor memory is freed
-            if (one)
-                mma_commit<kPair>(smem_addr(&s_drain));
-            mbar_wait(smem_addr(&s_drain), 0, nullptr);
         }
     } else if (warp < kResultWarps) {
         // ---- results
@@ -754,8 +774,33 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     __syncwarp();
     fence_before_sync();
     __syncthreads();
-    if constexpr (kPair)
+    bool lost = s_dead != 0;
+    if constexpr (kPair) {
+        if (threadIdx.x == 0) {  // what either CTA has to know of the other
+            s_lost[rank] = lost;
+            shared_store_peer(peer_addr(smem_addr(&s_lost[rank]), rank ^ 1), lost);
+            shared_store_peer(peer_addr(smem_addr(&s_steps[rank]), rank ^ 1), s_steps[rank]);
+        }
+        __syncwarp();
         cluster_sync();  // no CTA leaves while its pair may still signal it
+        lost = (s_lost[0] | s_lost[1]) != 0;
+    }
+    if (lost) {
+        // loads and products in flight end before shared and tensor memory are given up
+        if (warp == kResultWarps && rank == 0) {
+            drain_loads<kPair, S::kStages>(smem_addr(s_full), s_steps[0], s_steps[kPair ? 1 : 0],
+                                           kBytesA + g.job[0].tn / S::kCtas * (kTileK * 2), lane);
+        } else if (warp == kResultWarps + 1) {
+            if (rank == 0 && elect_one())
+                mma_commit<kPair>(smem_addr(&s_drain));
+            __syncwarp();
+            mbar_wait(smem_addr(&s_drain), 0, nullptr);
+        }
+        __syncwarp();
+        __syncthreads();
+        if constexpr (kPair)
+            cluster_sync();
+    }
     fence_after_sync();
     if (warp == 0)
         tmem_free<kPair>(tmem, 512);
@@ -1486,9 +1531,13 @@ cudaError_t launch_few(const GemmArgs& g, const mpt_xent_args& a, const Plan& p,
                               static_cast<const uint16_t*>(a.weight), a.ld_weight);
 }
 
+// What mpt_debug_xent_give_up asked of this thread's next call.
+thread_local int32_t t_give_up = 0;
+
 template <bool kPair, int kMode, bool kBf16>
 cudaError_t launch_shape(GemmArgs& g, cudaStream_t st)
 {
+    g.give_up = t_give_up >> kMode & 1;
     using S = Shape<kPair, kMode>;
     cudaLaunchConfig_t lc = {};
     const int32_t tiles = g.job[0].tiles + g.job[1].tiles;
@@ -1730,6 +1779,14 @@ int mpt_xent_args_init(mpt_xent_args* args)
     return MPT_OK;
 }
 
+int mpt_debug_xent_give_up(int32_t passes)
+{
+    if (passes & ~(MPT_XENT_PASS_LOSS | MPT_XENT_PASS_DZ | MPT_XENT_PASS_GRAD))
+        return MPT_ERR_INVALID_ARG;
+    t_give_up = passes;
+    return MPT_OK;
+}
+
 int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes)
 {
     if (!args_ok(args) || !bytes)
@@ -1760,6 +1817,9 @@ int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void
     }
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     char* ws = static_cast<char*>(d_workspace);
+    struct Once {
+        ~Once() { t_give_up = 0; }
+    } once;
     const int done = args->type == MPT_BF16 ? enqueue<true>(*args, p, ws, st) : enqueue<false>(*args, p, ws, st);
     if (done != MPT_OK)
         cudaGetLastError();  // this call's own error

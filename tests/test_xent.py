@@ -619,6 +619,33 @@ def test_offsets_beyond_31_bits(n):
            "grad_hidden")
 
 
+def test_the_hook_that_lets_waits_run_out():
+    L = lsf.lib()
+    assert L.mpt_debug_xent_give_up(8) == lsf.MPT_ERR_INVALID_ARG
+    assert L.mpt_debug_xent_give_up(7) == 0 and L.mpt_debug_xent_give_up(0) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("passes", [1, 2, 4, 7])
+@pytest.mark.parametrize("shape", [(100, 60001, 72), (700, 9000, 192), (300, 900, 1024)], ids=lambda s: "x".join(map(str, s)))
+def test_waits_that_run_out_end_the_call(shape, passes):
+    """One CTA to a tile, two, and logits kept: every block gives up where it
+    would wait, ends what it has in flight and leaves; the loss is NaN, and the
+    next call is whole."""
+    import torch
+    n, v, d = shape
+    h, w, t = _inputs(n, v, d, "float16", 28)
+    good = lsf.xent_grad(h, w, t, scale=16.0 * n)
+    for _ in range(4):
+        assert lsf.lib().mpt_debug_xent_give_up(passes) == 0
+        r = lsf.xent_grad(h, w, t, scale=16.0 * n)
+        torch.cuda.synchronize()
+        if passes != 2 or d < 1000:                # (2: kept logits are not multiplied again)
+            assert math.isnan(r.loss.item())
+    r = lsf.xent_grad(h, w, t, scale=16.0 * n)
+    assert all(torch.equal(a, b) for a, b in zip(r, good))
+
+
 def test_refusals_of_the_binding_on_the_cpu():
     import torch
     h, w, t = torch.zeros(4, 16).half(), torch.zeros(8, 16).half(), torch.zeros(4, dtype=torch.int64)
