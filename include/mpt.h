@@ -540,13 +540,18 @@ int mpt_xent_workspace_bytes(const mpt_xent_args* args, size_t* bytes);
  * workspace (256-byte aligned) holds nothing between calls: calls that may
  * overlap on the GPU need one each.  Can be captured into a CUDA graph; the
  * first call on a device loads the kernels, so make one before any capture.
+ * No wait inside a kernel is without a limit (some seconds, where none takes a
+ * millisecond): should one run out, the work still ends, the loss is NaN, and so
+ * is a value at least of every gradient that is not whole, so that mpt_step
+ * skips on it.
  * Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA; on an
  * argument error nothing is queued. */
 int mpt_xent(const mpt_xent_args* args, void* d_workspace, size_t ws_bytes, void* cuda_stream);
 
-/* Test hook: in the next mpt_xent that this thread queues, the waits inside the
- * named passes' product kernels give up at once where they would wait, as they
- * do after some seconds otherwise.  Errors: MPT_ERR_INVALID_ARG. */
+/* Test hook: in the next mpt_xent that this thread queues, the blocks of the
+ * named passes' product kernels stop loading after up to eight steps and give
+ * up the waits for what does not come, as they do after some seconds otherwise.
+ * Errors: MPT_ERR_INVALID_ARG. */
 #define MPT_XENT_PASS_LOSS 0x1 /* products of the loss (from five rows on)           */
 #define MPT_XENT_PASS_DZ 0x2   /* logits multiplied again (where they are not kept)  */
 #define MPT_XENT_PASS_GRAD 0x4 /* products of the gradients                          */

@@ -140,8 +140,8 @@ struct GemmArgs {
     float exponent;       // dz is scaled by 2^exponent
     // kGrad
     int32_t d;
-    float* poison;        // kDz, kGrad: a wait that ran out makes the loss NaN
-    int32_t give_up;      // test hook: as if a wait of every block had run out
+    float* poison;        // kDz, kGrad: the loss, NaN after a wait that ran out
+    int32_t give_up;      // test hook: each block gives up after its first loads
 };
 
 __device__ __forceinline__ int64_t target_of(const GemmArgs& g, int row)
@@ -512,6 +512,33 @@ __device__ __forceinline__ void drain_loads(uint32_t full, uint32_t steps0, uint
     }
 }
 
+// After a wait that ran out a block's tiles may be missing: NaN goes where they
+// are, or into what everything else is made from, so that neither a loss nor a
+// gradient that is not whole looks like one that is (an optimizer step sees the
+// gradients only).  The block's own stores are done.
+template <int kTileM, int kMode>
+__device__ __forceinline__ void poison_results(const GemmArgs& g, int worker, int workers, uint32_t rank)
+{
+    const float nan = __int_as_float(0x7fc00000);
+    if (kMode != kLoss && threadIdx.x == 0) {
+        *g.poison = nan;
+        g.control->gscale = nan;  // sums that are not rounded yet, later pieces
+    }
+    for (int k = 0, t; (t = tile_number(g, worker, workers, k)) >= 0; ++k) {
+        const Tile u = tile_at(g, t);
+        const int row0 = u.m * kTileM + (int)rank * kRows;
+        if constexpr (kMode == kLoss) {
+            const int row = row0 + (int)threadIdx.x % kRows, half = (int)threadIdx.x / kRows;
+            if (half < 2 && row < g.n)
+                g.part[(int64_t)row * g.part_ld + 2 * u.n + half] = make_float2(nan, nan);
+        } else if constexpr (kMode == kGrad) {
+            const Job& j = g.job[u.job];
+            if (j.final && threadIdx.x == 0 && row0 < j.rows && u.n * u.tn < g.d)
+                j.to[(int64_t)row0 * j.ld + u.n * u.tn] = 0x7FFF;  // NaN in either type
+        }
+    }
+}
+
 template <bool kPair, int kMode, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ GemmArgs g)
 {
@@ -574,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         // ---- loads: this CTA's rows of A and its share of the columns of B
         Ring<S::kStages> ring;
         uint32_t steps = 0;
+        const uint32_t stop = g.give_up ? (worker * 2 + rank * 3) % 9 : ~0u;  // either CTA of a pair elsewhere
         bool ok = true;
         const bool one = elect_one();
         for (int k = 1; ok && more; ++k, more = after, u = then) {
@@ -585,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             const uint32_t bytes = (kBytesA + share * (kTileK * 2)) * S::kCtas;
             auto run = [&](auto a_mn, auto b_mn) {
                 for (int kb = u.kb0; kb < u.kb1; ++kb, ++steps, ring.next()) {
-                    if (!(ok = mbar_wait_warp(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead)))
+                    ok = steps != stop && mbar_wait_warp(smem_addr(s_empty) + ring.at * 8, ring.phase ^ 1, dead);
+                    if (!ok)
                         break;
                     if (one) {
                         uint32_t full = smem_addr(s_full) + ring.at * 8;
@@ -804,12 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     fence_after_sync();
     if (warp == 0)
         tmem_free<kPair>(tmem, 512);
-    if (threadIdx.x == 0) {
-        if constexpr (kMode == kLoss)
-            g.control->status[blockIdx.x] = s_dead;
-        else if (s_dead)
-            *g.poison = __int_as_float(0x7fc00000);
-    }
+    if (kMode == kLoss && threadIdx.x == 0)
+        g.control->status[blockIdx.x] = lost;
+    if (lost)
+        poison_results<S::kTileM, kMode>(g, worker, workers, rank);
 }
 
 // ---------------------------------------------------------------------------
@@ -1160,7 +1187,7 @@ xent_merge_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ Me
         if (a.n_valid)
             *a.n_valid = (int64_t)count;
         const double S = (double)(a.d_scale ? *a.d_scale : a.scale);
-        g.control->gscale = (float)ldexp(S / by, -(int)g.exponent);
+        g.control->gscale = s_bad ? __int_as_float(0x7fc00000) : (float)ldexp(S / by, -(int)g.exponent);
     }
 }
 

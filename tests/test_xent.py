@@ -646,6 +646,53 @@ def test_waits_that_run_out_end_the_call(shape, passes):
     assert all(torch.equal(a, b) for a, b in zip(r, good))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("passes", [1, 2, 4])
+@pytest.mark.parametrize("shape", [(100, 60001, 72), (700, 9000, 192), (300, 900, 1024), (17_000, 700, 72),
+                                   (4000, 40_000, 64)], ids=lambda s: "x".join(map(str, s)))
+def test_no_gradient_looks_whole_after_a_wait_that_ran_out(shape, passes):
+    """Sums cut, results final, logits kept, cuts of the rows, two pieces."""
+    import torch
+    n, v, d = shape
+    if passes == 2 and shape == (300, 900, 1024):
+        return                                     # kept logits are not multiplied again
+    h, w, t = _inputs(n, v, d, "float16", 29)
+    for kw in (dict(), dict(grad_hidden=None), dict(grad_weight=None)):
+        good = lsf.xent_grad(h, w, t, scale=16.0 * n, **kw)
+        grads = {k: torch.full_like(x, 3.0) for k, x in good._asdict().items() if k.startswith("grad") and x is not None}
+        assert lsf.lib().mpt_debug_xent_give_up(passes) == 0
+        r = lsf.xent_grad(h, w, t, scale=16.0 * n, **(kw | grads))
+        assert math.isnan(r.loss.item())
+        if passes == 1:
+            assert bool(torch.isnan(r.token_loss[t != IGNORE]).all()) and bool(torch.isnan(r.lse).all())
+        for name, x in grads.items():
+            nan = torch.isnan(x)
+            assert bool(nan.any()) if passes == 4 else bool(nan.all()), name
+
+
+@pytest.mark.gpu
+def test_a_step_skips_after_a_wait_that_ran_out():
+    import torch
+    v, d, n = 1000, 128, 200
+    h, w0, t = _inputs(n, v, d, "float16", 30)
+    opt = lsf.MPT([v * d], lsf.Config())
+    opt.master(0).copy_(w0.float().flatten())
+    opt.refresh_half()
+    opt.set_scaler_state(64.0)
+    grad = torch.zeros(v * d, dtype=torch.float16, device="cuda")
+    before = opt.master(0).clone()
+    for passes in (1, 4):
+        assert lsf.lib().mpt_debug_xent_give_up(passes) == 0
+        opt.head_grad(0, h, t, grad_weight=grad.view(v, d))
+        opt.step_async([grad], 0.5, 0.0, 0.0)
+        assert opt.wait()["found_inf"] == 1
+        assert torch.equal(opt.master(0), before)
+    opt.head_grad(0, h, t, grad_weight=grad.view(v, d))
+    opt.step_async([grad], 0.5, 0.0, 0.0)
+    assert opt.wait()["found_inf"] == 0 and not torch.equal(opt.master(0), before)
+    opt.close()
+
+
 def test_refusals_of_the_binding_on_the_cpu():
     import torch
     h, w, t = torch.zeros(4, 16).half(), torch.zeros(8, 16).half(), torch.zeros(4, dtype=torch.int64)
