@@ -215,6 +215,14 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _check_stream(stream, device):
+    """A stream of another device would run the work there, on this one's
+    addresses."""
+    import torch
+    if stream is not None and torch.device(stream.device) != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+
+
 def _on(device, stream):
     """A context in which ``device`` (and ``stream``, if given) are current."""
     import torch
@@ -498,6 +506,7 @@ class GradList:
     def norm(self, grads, scale=1.0, clip=0.0, tensor_norms=False, stream=None):
         """Queue the norm of ``grads`` (CUDA tensors, or an array from
         :func:`grad_pointers`); ``clip`` only sets the ``coef`` reported."""
+        _check_stream(stream, self.device)
         host, dev = _scale_args(scale, self.device)
         g = self._ptrs(grads, self.dtypes, "gradient")
         if stream is not None:
@@ -511,6 +520,7 @@ class GradList:
     def clip(self, grads, clip, out=None, scale=1.0, unscale=False, tensor_norms=False, stream=None):
         """Queue the norm and the scaling of ``grads`` to a norm of at most
         ``clip``, into ``out`` (default: in place)."""
+        _check_stream(stream, self.device)
         host, dev = _scale_args(scale, self.device)
         g = self._ptrs(grads, self.dtypes, "gradient")
         if out is None and self.out_dtypes != self.dtypes:
@@ -575,6 +585,7 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
         raise ValueError("targets must be one int32 or int64 per row of hidden, contiguous, on its device")
     if reduction not in ("mean", "sum"):
         raise ValueError("reduction is 'mean' or 'sum'")
+    _check_stream(stream, dev)
     host_scale, dev_scale = _scale_args(scale, dev)
     if stream is not None:
         _used_on(stream, hidden, weight, targets, scale, grad_hidden, grad_weight)

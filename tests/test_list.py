@@ -76,6 +76,19 @@ def test_null_lists_and_host_workspaces_are_refused():
     assert L.mpt_list_create(one, t, None, 1, None, 1 << 15, ctypes.byref(h)) == lsf.MPT_ERR_WORKSPACE
 
 
+def test_a_stream_of_another_device_is_refused():
+    """With a stand-in for the stream and a list that has nothing behind it:
+    refused before anything is looked at."""
+    import torch
+    import types
+    lst = lsf.GradList.__new__(lsf.GradList)
+    lst.device = torch.device("cuda", 0)
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    for call in (lambda: lst.norm([], stream=other), lambda: lst.clip([], 1.0, stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
 # ---------------------------------------------------------------------------
 # GPU
 # ---------------------------------------------------------------------------

@@ -702,6 +702,19 @@ def test_refusals_of_the_binding_on_the_cpu():
 
 
 @pytest.mark.gpu
+def test_a_stream_of_another_device_is_refused():
+    """With a stand-in for the stream: refused before it is used at all."""
+    import torch
+    import types
+    h, w, t = _inputs(10, 50, 64, "float16", 31)
+    other = types.SimpleNamespace(device=torch.device("cuda", h.device.index + 1))
+    with pytest.raises(ValueError, match="stream"):
+        lsf.xent_loss(h, w, t, stream=other)
+    with pytest.raises(ValueError, match="stream"):
+        lsf.xent_grad(h, w, t, stream=other)
+
+
+@pytest.mark.gpu
 def test_refusals_of_the_binding():
     import torch
     h, w, t = _inputs(10, 50, 64, "float16", 18)
