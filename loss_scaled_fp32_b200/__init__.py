@@ -536,9 +536,11 @@ class GradList:
 
     def wait(self, stream=None):
         """Wait for the queued work; the last result as a dict of numbers."""
+        _check_stream(stream, self.device)
         r = CheckResult()
-        _check(lib().mpt_list_wait(self._h, _stream_ptr(stream, self.device), ctypes.byref(r)),
-               "mpt_list_wait")
+        with _on(self.device, stream):
+            _check(lib().mpt_list_wait(self._h, _stream_ptr(stream, self.device), ctypes.byref(r)),
+                   "mpt_list_wait")
         return r.as_dict()
 
     def close(self):

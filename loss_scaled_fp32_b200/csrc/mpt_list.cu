@@ -1067,6 +1067,11 @@ int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out)
         return MPT_ERR_INVALID_ARG;
     if (h->broken)
         return MPT_ERR_BROKEN;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return fail_cuda(h);
+    if (dev != h->device)  // whose default stream would be waited for
+        return MPT_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     if (cudaMemcpyAsync(h->mailbox, h->ws + h->p.off_result, sizeof(mpt_check_result),
                         cudaMemcpyDeviceToHost, st) != cudaSuccess ||

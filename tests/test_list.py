@@ -89,6 +89,31 @@ def test_a_stream_of_another_device_is_refused():
             call()
 
 
+def test_wait_makes_the_lists_device_current(monkeypatch):
+    """Otherwise a list on the default stream of another device than the
+    current one would wait for the current one's."""
+    import contextlib
+    import torch
+    import types
+    lst = lsf.GradList.__new__(lsf.GradList)
+    lst.device, lst._h = torch.device("cuda", 1), ctypes.c_void_p()
+    inside = []
+
+    @contextlib.contextmanager
+    def on(device, stream):
+        inside.append(device)
+        yield
+        inside.pop()
+    seen = []
+    fake = types.SimpleNamespace(mpt_list_wait=lambda *a: seen.append(list(inside)) or 0)
+    monkeypatch.setattr(lsf, "_on", on)
+    monkeypatch.setattr(lsf, "_stream_ptr", lambda stream, device: ctypes.c_void_p())
+    monkeypatch.setattr(lsf, "lib", lambda: fake)
+    lst.wait()
+    assert seen == [[lst.device]]
+    lst._h = None
+
+
 # ---------------------------------------------------------------------------
 # GPU
 # ---------------------------------------------------------------------------
