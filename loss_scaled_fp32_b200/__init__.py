@@ -444,7 +444,8 @@ class GradList:
     1-element float32 CUDA tensor such as :meth:`MPT.device_scale`.  The calls
     return views of the list's own result buffers, which the next call
     overwrites: ``norm`` (float64), ``coef`` (float32), ``found_inf`` (int32),
-    ``n_nonfinite`` (int64), and ``tensor_norms`` (float64) if asked.
+    ``n_nonfinite`` (int64), and ``tensor_norms`` (float64) if asked.  A list may
+    be dropped while its calls run, but not while a graph that captured one lives.
     """
 
     def __init__(self, sizes, dtypes, out_dtypes=None, device=None):
@@ -462,6 +463,7 @@ class GradList:
         nbytes = ctypes.c_size_t()
         _check(lib().mpt_list_workspace_bytes(*args, ctypes.byref(nbytes)), "mpt_list_workspace_bytes")
         self.workspace = torch.empty(nbytes.value, dtype=torch.uint8, device=self.device)
+        self._streams = {_stream_ptr(None, self.device).value}  # that the allocator knows to use it
         self._h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
             _check(lib().mpt_list_create(*args, ctypes.c_void_p(self.workspace.data_ptr()), nbytes.value,
@@ -500,6 +502,17 @@ class GradList:
                 raise ValueError(f"{what} tensor does not match its size/dtype/device or is not contiguous")
         return grad_pointers(tensors)
 
+    def _queue_on(self, stream):
+        """The raw stream of a call.  The list may be dropped while the call
+        runs, so the allocator hears of any stream but the one that was current
+        at creation."""
+        import torch
+        raw = _stream_ptr(stream, self.device)
+        if raw.value not in self._streams:
+            _used_on(stream if stream is not None else torch.cuda.current_stream(self.device), self.workspace)
+            self._streams.add(raw.value)
+        return raw
+
     def _views(self, tensor_norms):
         return self._result | {"tensor_norms": self._tensor_norms} if tensor_norms else dict(self._result)
 
@@ -514,7 +527,7 @@ class GradList:
         with _on(self.device, stream):
             _check(lib().mpt_list_norm(self._h, g, host, dev, clip,
                                        MPT_LIST_TENSOR_NORMS if tensor_norms else 0,
-                                       _stream_ptr(stream, self.device)), "mpt_list_norm")
+                                       self._queue_on(stream)), "mpt_list_norm")
         return self._views(tensor_norms)
 
     def clip(self, grads, clip, out=None, scale=1.0, unscale=False, tensor_norms=False, stream=None):
@@ -530,8 +543,7 @@ class GradList:
             _used_on(stream, scale, *(() if g is grads else grads), *(() if out is None or o is out else out))
         flags = (MPT_LIST_TENSOR_NORMS if tensor_norms else 0) | (MPT_LIST_UNSCALE if unscale else 0)
         with _on(self.device, stream):
-            _check(lib().mpt_list_clip(self._h, g, o, host, dev, clip, flags,
-                                       _stream_ptr(stream, self.device)), "mpt_list_clip")
+            _check(lib().mpt_list_clip(self._h, g, o, host, dev, clip, flags, self._queue_on(stream)), "mpt_list_clip")
         return self._views(tensor_norms)
 
     def wait(self, stream=None):

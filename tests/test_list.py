@@ -114,6 +114,28 @@ def test_wait_makes_the_lists_device_current(monkeypatch):
     lst._h = None
 
 
+def test_the_allocator_hears_of_every_stream_that_uses_the_workspace(monkeypatch):
+    import contextlib
+    import torch
+    import types
+    lst = lsf.GradList.__new__(lsf.GradList)
+    lst.device, lst._h, lst.n, lst.sizes = torch.device("cuda", 0), None, 1, [1]
+    lst.dtypes = lst.out_dtypes = [torch.float16]
+    lst.workspace, lst._result, lst._streams = torch.zeros(8, dtype=torch.uint8), {}, {16}
+    told = []
+    monkeypatch.setattr(lsf, "_on", lambda device, stream: contextlib.nullcontext())
+    monkeypatch.setattr(lsf, "_used_on", lambda stream, *ts: told.append(stream) if any(t is lst.workspace for t in ts) else None)
+    monkeypatch.setattr(lsf, "lib", lambda: types.SimpleNamespace(mpt_list_norm=lambda *a: 0, mpt_list_clip=lambda *a: 0))
+    home, other, third = (types.SimpleNamespace(device=lst.device, cuda_stream=k) for k in (16, 32, 48))
+    ptrs = lsf.grad_pointers([torch.zeros(1)])
+    lst.norm(ptrs, stream=home)
+    assert told == []
+    lst.norm(ptrs, stream=other)
+    lst.clip(ptrs, 1.0, stream=other)
+    lst.clip(ptrs, 1.0, stream=third)
+    assert told == [other, third]
+
+
 # ---------------------------------------------------------------------------
 # GPU
 # ---------------------------------------------------------------------------
@@ -400,3 +422,38 @@ def test_clip_then_step_is_the_step_that_clips():
         assert bool(((opts[0].master(i) - opts[1].master(i)).double().abs() <= far).all())
     for o in opts:
         o.close()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("explicit", [True, False])
+def test_a_list_dropped_while_its_call_runs_keeps_its_workspace(explicit):
+    """A call on another stream than the list's own, the list dropped at once:
+    its workspace is not handed out again before the call is done."""
+    import torch
+    sizes = [40_000, 7]
+    tensors = _tensors(sizes, [F16] * 2, 41)
+    want = [t.clone() for t in tensors]
+    twin = lsf.GradList(sizes, torch.float16)
+    coef = twin.clip(want, 1e-4)["coef"].item()
+    assert coef < 1.0
+    side = torch.cuda.Stream()
+    lst = lsf.GradList(sizes, torch.float16)
+    lst.clip(tensors, 1e9)                        # nothing to clip; the pointers are on the device now
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)            # some 0.1 s
+    kept = lst.workspace.data_ptr()
+    if explicit:
+        lst.clip(tensors, 1e-4, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            lst.clip(tensors, 1e-4)
+    done = side.record_event()
+    nbytes = lst.workspace.numel()
+    lst = None
+    running = not done.query()                    # (unless dropping the list has waited for it)
+    again = [torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert not running or all(x.data_ptr() != kept for x in again)
+    torch.cuda.synchronize()
+    for t, w in zip(tensors, want):
+        assert _same(t, w)
