@@ -472,7 +472,9 @@ int mpt_list_views(const mpt_list* h, mpt_check_result** d_result, double** d_te
  * current), MPT_ERR_CUDA, MPT_ERR_BROKEN. */
 int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out);
 
-/* Release the list's host resources (NULL is accepted). */
+/* Release the list's host resources (NULL is accepted), once the copies of
+ * pointer tables that its calls have queued are done.  The workspace has to stay
+ * until the kernels are. */
 int mpt_list_destroy(mpt_list* h);
 
 /* ---- softmax cross entropy of a head, with loss-scaled gradients ---------

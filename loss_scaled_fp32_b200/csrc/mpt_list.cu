@@ -725,8 +725,11 @@ void release(mpt_list* h)
     if (!h)
         return;
     for (auto& s : h->slot) {
-        if (s.copied)
+        if (s.copied) {
+            if (cudaEventSynchronize(s.copied) != cudaSuccess)  // the copy reads s.pinned
+                cudaGetLastError();
             cudaEventDestroy(s.copied);
+        }
         if (s.pinned)
             cudaFreeHost(s.pinned);
     }

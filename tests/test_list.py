@@ -457,3 +457,17 @@ def test_a_list_dropped_while_its_call_runs_keeps_its_workspace(explicit):
     torch.cuda.synchronize()
     for t, w in zip(tensors, want):
         assert _same(t, w)
+
+
+@pytest.mark.gpu
+def test_closing_waits_for_the_copy_of_a_new_table():
+    import torch
+    tensors = _tensors([1000], [F16], 42)
+    lst = lsf.GradList([1000], torch.float16)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    before = torch.cuda.current_stream().record_event()
+    r = lst.norm(tensors, tensor_norms=True)
+    lst.close()
+    assert before.query()
+    _check(r, tensors, 1.0, 0.0)
