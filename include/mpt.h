@@ -468,8 +468,8 @@ int mpt_list_clip(mpt_list* h, const void* const* d_grads, void* const* d_out, f
 int mpt_list_views(const mpt_list* h, mpt_check_result** d_result, double** d_tensor_norms);
 
 /* Wait for the work queued on cuda_stream and return the last result (out
- * may be NULL).  Errors: MPT_ERR_INVALID_ARG (also: another device is
- * current), MPT_ERR_CUDA, MPT_ERR_BROKEN. */
+ * may be NULL).  Errors: MPT_ERR_INVALID_ARG (also: another device is current;
+ * cuda_stream is being captured), MPT_ERR_CUDA, MPT_ERR_BROKEN. */
 int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out);
 
 /* Release the list's host resources (NULL is accepted), once the copies of

@@ -789,17 +789,26 @@ int fail_cuda(mpt_list* h)
     return MPT_ERR_CUDA;
 }
 
+// Whether the stream is being captured; false if it cannot be told.
+bool is_capturing(cudaStream_t st, bool* capturing)
+{
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
+        cudaGetLastError();  // the default stream while another one is captured: nothing was queued
+        return false;
+    }
+    *capturing = cap != cudaStreamCaptureStatusNone;
+    return true;
+}
+
 // The slot that holds this pointer table on the device.
 int find_slot(mpt_list* h, const void* const* grads, void* const* outs, cudaStream_t st, int* out)
 {
     const int32_t n = h->n;
     const size_t half = sizeof(void*) * (size_t)n;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) {
-        cudaGetLastError();  // the default stream while another one is captured: nothing was queued
+    bool capturing = false;
+    if (!is_capturing(st, &capturing))
         return MPT_ERR_CUDA;
-    }
-    const bool capturing = cap != cudaStreamCaptureStatusNone;
     // a norm finds its gradients in a clipping's table too; the slot used last
     // is looked at first
     int k = -1;
@@ -1076,6 +1085,11 @@ int mpt_list_wait(mpt_list* h, void* cuda_stream, mpt_check_result* out)
     if (dev != h->device)  // whose default stream would be waited for
         return MPT_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    bool capturing = false;
+    if (!is_capturing(st, &capturing))
+        return MPT_ERR_CUDA;
+    if (capturing)
+        return MPT_ERR_INVALID_ARG;  // nothing runs that could be waited for
     if (cudaMemcpyAsync(h->mailbox, h->ws + h->p.off_result, sizeof(mpt_check_result),
                         cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)

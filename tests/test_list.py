@@ -471,3 +471,26 @@ def test_closing_waits_for_the_copy_of_a_new_table():
     lst.close()
     assert before.query()
     _check(r, tensors, 1.0, 0.0)
+
+
+@pytest.mark.gpu
+def test_waiting_inside_a_capture_is_refused():
+    """The capture goes on, and the list stays usable."""
+    import torch
+    tensors = _tensors([1000], [F16], 43)
+    lst = lsf.GradList([1000], torch.float16)
+    lst.norm(tensors)
+    x = torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1.0)
+        r = lst.norm(tensors, tensor_norms=True)
+        with pytest.raises(lsf.MptError) as e:
+            lst.wait()
+        assert e.value.code == lsf.MPT_ERR_INVALID_ARG
+    g.replay()
+    torch.cuda.synchronize()
+    assert x[0].item() == 1.0
+    _check(r, tensors, 1.0, 0.0)
+    assert lst.wait()["grad_norm"] == r["norm"].item()
