@@ -724,6 +724,10 @@ void release(mpt_list* h)
 {
     if (!h)
         return;
+    // a list may go while this thread captures something else (Python frees one
+    // when it likes): nothing here touches a stream
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
     for (auto& s : h->slot) {
         if (s.copied) {
             if (cudaEventSynchronize(s.copied) != cudaSuccess)  // the copy reads s.pinned
@@ -735,6 +739,8 @@ void release(mpt_list* h)
     }
     if (h->mailbox)
         cudaFreeHost(h->mailbox);
+    if (relaxed)
+        cudaThreadExchangeStreamCaptureMode(&mode);
     delete h;
 }
 

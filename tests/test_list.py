@@ -494,3 +494,21 @@ def test_waiting_inside_a_capture_is_refused():
     assert x[0].item() == 1.0
     _check(r, tensors, 1.0, 0.0)
     assert lst.wait()["grad_norm"] == r["norm"].item()
+
+
+@pytest.mark.gpu
+def test_a_list_that_goes_during_a_capture_leaves_it_alone():
+    import torch
+    tensors = _tensors([1000], [F16], 44)
+    lst = lsf.GradList([1000], torch.float16)
+    lst.norm(tensors)
+    x = torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1.0)
+        lst.close()
+        x.add_(1.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert x[0].item() == 2.0
