@@ -430,8 +430,9 @@ int mpt_list_workspace_bytes(const int64_t* sizes, const int32_t* types, const i
                              int32_t n, size_t* bytes);
 
 /* Create a list over a caller-owned device workspace (256-byte aligned, at
- * least mpt_list_workspace_bytes), synchronously; the workspace must outlive
- * the list.  Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA. */
+ * least mpt_list_workspace_bytes), synchronously, after all work queued on the
+ * device (so not while a stream is captured); the workspace must outlive the
+ * list.  Errors: MPT_ERR_INVALID_ARG, MPT_ERR_WORKSPACE, MPT_ERR_CUDA. */
 int mpt_list_create(const int64_t* sizes, const int32_t* types, const int32_t* out_types, int32_t n,
                     void* d_workspace, size_t ws_bytes, mpt_list** out);
 

@@ -1018,7 +1018,9 @@ int mpt_list_create(const int64_t* sizes, const int32_t* types, const int32_t* o
         return bytes == 0 || cudaMemcpy(to, from, bytes, cudaMemcpyHostToDevice) == cudaSuccess;
     };
     cudaFuncAttributes fa;  // loads the kernels, so that no later call loads code inside a capture
-    bool ok = cudaFuncGetAttributes(&fa, list_norm_kernel<false>) == cudaSuccess &&
+    // the workspace may come from a stream that still writes what was there before
+    bool ok = cudaDeviceSynchronize() == cudaSuccess &&
+              cudaFuncGetAttributes(&fa, list_norm_kernel<false>) == cudaSuccess &&
               cudaFuncGetAttributes(&fa, list_norm_kernel<true>) == cudaSuccess &&
               cudaFuncGetAttributes(&fa, list_clip_kernel) == cudaSuccess &&
               cudaFuncGetAttributes(&fa, list_finish_kernel) == cudaSuccess &&

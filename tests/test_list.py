@@ -512,3 +512,26 @@ def test_a_list_that_goes_during_a_capture_leaves_it_alone():
     g.replay()
     torch.cuda.synchronize()
     assert x[0].item() == 2.0
+
+
+@pytest.mark.gpu
+def test_a_workspace_that_is_still_written_by_its_last_owner():
+    """The allocator hands out memory in stream order: what the stream's earlier
+    work still writes there comes before the list's tables."""
+    import torch
+    sizes = [40_000, 7]
+    tensors = _tensors(sizes, [F16] * 2, 45)
+    nbytes = lsf.GradList(sizes, torch.float16).workspace.numel()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        at = x.data_ptr()
+        torch.cuda._sleep(200_000_000)            # some 0.1 s
+        x.fill_(0)
+        x = None
+        lst = lsf.GradList(sizes, torch.float16)
+        assert lst.workspace.data_ptr() == at
+        r = lst.norm(tensors, tensor_norms=True)
+    torch.cuda.synchronize()
+    _check(r, tensors, 1.0, 0.0)
