@@ -579,7 +579,7 @@ def _rows(t, what, dtype, device, shape=None):
     (n, d), (ld, step) = t.shape, t.stride()
     if step != 1 and d > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    return ld if n > 1 else max(ld, (d + 7) // 8 * 8)
+    return ld if n > 1 else (d + 7) // 8 * 8  # one row has no next
 
 
 def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, grad_weight, stream):

@@ -257,6 +257,33 @@ def test_rows_with_gaps_and_unaligned_gradients(n):
             assert bool((room[keep] == 3.0).all())
 
 
+def test_the_row_distance_of_one_row_is_not_looked_at():
+    """A row cut out of a matrix of any width is a matrix like any other."""
+    import torch
+    cpu = torch.device("cpu")
+    x = torch.zeros(3, 1001, dtype=torch.float16)
+    assert lsf._rows(x[1:2, :64], "hidden", torch.float16, cpu) == 64
+    assert lsf._rows(x[:, :64], "hidden", torch.float16, cpu) == 1001
+    assert lsf._rows(torch.zeros(1, 64, dtype=torch.float16).expand(1, 64), "hidden", torch.float16, cpu) == 64
+
+
+@pytest.mark.gpu
+def test_one_row_of_a_matrix_of_any_width():
+    import torch
+    h, w, t = _inputs(1, 300, 64, "float16", 32, ignored=0.0)
+    ref = _reference(h, w, t, 16.0)
+    room = [torch.full((2, 1001), 3.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    room[0][:1, :64] = h
+    gh = room[1][:1, :64]
+    r = lsf.xent_grad(room[0][:1, :64], w, t, scale=16.0, grad_hidden=gh)
+    _check(r, ref)
+    assert r.grad_hidden is gh and bool((room[1][:, 64:] == 3.0).all()) and bool((room[1][1:] == 3.0).all())
+    one = torch.full((2, 1001), 3.0, dtype=torch.float16, device="cuda")[:1, :64]   # a head of one class
+    one.copy_(w[:1])
+    r = lsf.xent_grad(h, one, torch.zeros_like(t))
+    assert r.loss.item() == 0.0 and not r.grad_weight.any()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("n", [1, 4, 60, 300])
 def test_nothing_left_to_learn(n):
