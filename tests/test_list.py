@@ -535,3 +535,19 @@ def test_a_workspace_that_is_still_written_by_its_last_owner():
         r = lst.norm(tensors, tensor_norms=True)
     torch.cuda.synchronize()
     _check(r, tensors, 1.0, 0.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,bits", [(F16, 0x7C01), (BF16, 0x7F81), (F32, 0x7F800001)])
+def test_gradients_that_are_left_are_not_rewritten(kind, bits):
+    """Signalling NaN of a payload that widening and rounding change: the bits
+    stay where an overflow or the limit leaves the gradients, in place."""
+    import torch
+    ints = {2: torch.int16, 4: torch.int32}[_dtype(kind).itemsize]
+    (x,) = _tensors([70_001], [kind], 46)
+    x.view(ints)[69_998] = bits
+    x.view(ints)[5] = bits
+    before = x.view(ints).clone()
+    lst = lsf.GradList([70_001], _dtype(kind))
+    assert lst.clip([x], 1e-6)["n_nonfinite"].item() == 2
+    assert torch.equal(x.view(ints), before)

@@ -285,6 +285,39 @@ def test_one_row_of_a_matrix_of_any_width():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(3, 5003, 200), (50, 5003, 200), (200, 5003, 200), (4000, 33536 + 70, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_unaligned_gradients_of_cut_sums_and_pieces(shape):
+    """dH in five parts, written row by row at odd distances; the last shape has
+    a second piece of two blocks, fewer than the parts, whose dW starts in the
+    middle of an unaligned matrix."""
+    import torch
+    n, v, d = shape
+    h, w, t = _inputs(n, v, d, "float16", 33)
+    ref = _reference(h, w, t, 16.0 * n)
+    for extra, shift in ((1, 0), (3, 5), (8, 8), (8, 1)):
+        ld = d + extra
+        rooms = [torch.full((rows * ld + 16,), 3.0, dtype=torch.float16, device="cuda") for rows in (n, v)]
+        gh, gw = (room[shift:shift + rows * ld].view(rows, ld)[:, :d] for room, rows in zip(rooms, (n, v)))
+        _check(lsf.xent_grad(h, w, t, scale=16.0 * n, grad_hidden=gh, grad_weight=gw), ref)
+        for room, rows in zip(rooms, (n, v)):
+            keep = torch.ones_like(room, dtype=torch.bool)
+            keep[shift:shift + rows * ld].view(rows, ld)[:, :d] = False
+            assert bool((room[keep] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["float16", "bfloat16"])
+def test_a_last_piece_of_fewer_blocks_than_parts(kind):
+    n, v, d = 4000, 33536 + 70, 64
+    h, w, t = _inputs(n, v, d, kind, 34)
+    scale = 16.0 * n if kind == "float16" else 1.0
+    ref = _reference(h, w, t, scale)
+    _check(lsf.xent_grad(h, w, t, scale=scale), ref)
+    _check(lsf.xent_grad(h, w, t, scale=scale, grad_weight=None), ref)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [1, 4, 60, 300])
 def test_nothing_left_to_learn(n):
     """Every row ignored; no row at all."""
