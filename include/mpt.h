@@ -483,24 +483,33 @@ int mpt_list_destroy(mpt_list* h);
  * The start of the backward pass: the loss that S multiplies.  For n rows of
  * hidden (n x d), a head's weight (v x d) and one target class per row,
  *
- *   z      = hidden weight^T        (no buffer grows to this size: at most
- *                                    256 MB of it are held at once)
+ *   z      = hidden weight^T
  *   loss_i = log(sum_u exp(z_iu)) - z_it        (0 where t == ignore_index)
  *   loss   = sum of loss_i, or that divided by the number of rows that are
  *            not ignored (MPT_XENT_MEAN; 0 where every row is)
  *   grad_hidden = S dloss/dhidden,  grad_weight = S dloss/dweight
  *
  * FP16 or BF16 operands and gradients of the same type; products are summed
- * in binary32, exponentials and their sums are binary32, the gradient of the
+ * in binary32 (in parts of 512 for a logit, of at most 16384 for a gradient),
+ * exponentials and their sums are binary32, the gradient of the
  * logits is rounded to 16 bits once (scaled so that it does not underflow),
  * and S/n is applied in binary32 before the gradients are rounded: a value
  * beyond FP16's range becomes inf there, which mpt_step finds and skips on.
  * A target that is neither ignored nor a class makes the loss and the
  * gradients NaN (and nothing out of range is read), and so does a logit of
  * +inf or NaN, as an overflow in the layers below leaves it; one of -inf is a
- * class of probability 0 (as target: a loss of +inf).  Rows that are ignored
- * have to be finite, too: grad_weight adds 0 times them.  Each result depends on
+ * class of probability 0 (as target: a loss of +inf).  An infinite or NaN
+ * operand also spoils the gradient values that it is a factor of, by 0 too:
+ * rows that are ignored have to be finite.  Each result depends on
  * the call's arguments alone, bit for bit: no sum's order depends on timing. */
+/* Memory: no buffer holds all logits of a large call.  Their gradient is held for
+ * a piece of the vocabulary at a time, at most 256 MB in 16 bits; the logits of
+ * a call are kept only where all of them take at most 256 MB in binary32 and
+ * moving them is quicker than multiplying again.  The row statistics take a 64th
+ * of the logits in binary32, grad_hidden a binary32 copy for each part that its
+ * sums are cut into, and grad_weight, from 16385 rows on, one of a piece's
+ * classes.  The workspace does not always grow with n: ask for every size that
+ * is used. */
 #define MPT_XENT_MEAN 0
 #define MPT_XENT_SUM 1
 

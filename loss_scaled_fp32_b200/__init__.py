@@ -631,8 +631,7 @@ def _xent(hidden, weight, targets, scale, ignore_index, reduction, grad_hidden, 
 
 def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stream=None):
     """Softmax cross entropy of ``hidden @ weight.T`` against ``targets``
-    (``mpt_xent`` without gradients), queued; the logits are not stored (with
-    gradients, of at most 256 MB of them at a time).
+    (``mpt_xent`` without gradients), queued; the logits are not stored.
 
     Returns ``XentLoss``: ``loss`` (float32, 1 value), ``token_loss`` and
     ``lse`` (float32, one per row), ``n_valid`` (int64, 1 value)."""
@@ -641,7 +640,8 @@ def xent_loss(hidden, weight, targets, ignore_index=-100, reduction="mean", stre
 
 def xent_grad(hidden, weight, targets, scale=1.0, ignore_index=-100, reduction="mean", grad_hidden=True,
               grad_weight=True, stream=None):
-    """The same with the gradients of ``scale * loss`` (``mpt_xent``).
+    """The same with the gradients of ``scale * loss`` (``mpt_xent``).  At most
+    256 MB of the logits' gradient are held at a time, and up to 256 MB of logits.
 
     ``scale`` is S: a number, or a 1-element float32 CUDA tensor such as
     :meth:`MPT.device_scale`.  ``grad_hidden`` and ``grad_weight`` are tensors

@@ -6,7 +6,7 @@
 //   dz_iu  = exp(z_iu - lse_i) - [u = t]            (at u = t: expm1(-loss_i))
 //   dH = g dz W,  dW = g dz^T H,  g = S / valid rows (or S)
 //
-// No buffer grows to the logits' size.  The forward pass reduces each
+// No buffer holds all logits of a large call.  The forward pass reduces each
 // 256-column tile of z to a maximum and a sum per row while the next tile is
 // multiplied; the backward pass goes through the vocabulary in pieces: multiply
 // z again, write dz of the piece in 16 bits, and multiply it with W (dH, summed
