@@ -1339,9 +1339,9 @@ int64_t tile_columns(int64_t mt, int64_t cols, int64_t kb, int64_t workers, int6
 // them again.  Writing, reading and turning them into dz takes 1.4 ps each
 // (through memory); multiplying 2 d operations at 1.4 PFLOP/s, but no less than
 // reading the head at 6 TB/s, and 5 us more for a product kernel's start and
-// end.  With gradients, on the device: 77 x 1000 x 512 28 us again, 22 kept; 64 x
-// 50257 x 1024 122 and 105; 1001 x 50257 x 1024 351 and 342; the same at width
-// 512 231 and 258; 8192 x 1000 x 512 94 and 105.
+// end.  With gradients, on the device: 77 x 1000 x 512 25 us again, 21 kept; 64 x
+// 50257 x 1024 122 and 104; 1001 x 50257 x 1024 345 and 338; the same at width
+// 512 230 and 243; 8192 x 1000 x 512 85 and 85.
 bool keeping_pays(int64_t n, int64_t v, int64_t d)
 {
     const double logits = (double)n * (double)v;
