@@ -490,7 +490,9 @@ int mpt_list_destroy(mpt_list* h);
  *   grad_hidden = S dloss/dhidden,  grad_weight = S dloss/dweight
  *
  * FP16 or BF16 operands and gradients of the same type; products are summed
- * in binary32 (in parts of 512 for a logit, of at most 16384 for a gradient),
+ * in binary32 (in parts of 512 for a logit, of at most 16384 for a gradient;
+ * the tensor cores truncate, so that a logit whose products have one sign is low
+ * by up to 4e-6 of itself),
  * exponentials and their sums are binary32, the gradient of the
  * logits is rounded to 16 bits once (scaled so that it does not underflow),
  * and S/n is applied in binary32 before the gradients are rounded: a value
