@@ -492,9 +492,8 @@ int mpt_list_destroy(mpt_list* h);
  * FP16 or BF16 operands and gradients of the same type; products are summed
  * in binary32 (in parts of 512 for a logit, of at most 16384 for a gradient;
  * the tensor cores truncate, so that a logit whose products have one sign is low
- * by up to 4e-6 of itself),
- * exponentials and their sums are binary32, the gradient of the
- * logits is rounded to 16 bits once (scaled so that it does not underflow),
+ * by 2.4e-6 of itself), exponentials and their sums are binary32, the gradient of
+ * the logits is rounded to 16 bits once (scaled so that it does not underflow),
  * and S/n is applied in binary32 before the gradients are rounded: a value
  * beyond FP16's range becomes inf there, which mpt_step finds and skips on.
  * A target that is neither ignored nor a class makes the loss and the
